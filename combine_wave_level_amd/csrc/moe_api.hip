@@ -6,6 +6,7 @@
 #include <string.h>
 
 #include "moe_internal.h"
+#include "mxfp4.h"
 #include "wave_sched.h"
 
 namespace moe {
@@ -34,6 +35,13 @@ static moe_status_t check_problem(const moe_problem_t* p) {
   if (p->E_global > 256 || p->k > 64) return MOE_ERR_UNSUPPORTED;
   if (p->T > (1 << 24) || p->d > (1 << 16) || p->I > (1 << 16)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
+}
+
+// The MXFP4 products walk both reductions in steps of 128.
+static moe_status_t check_mx(const moe_problem_t* p) {
+  const moe_status_t st = check_problem(p);
+  if (st != MOE_OK) return st;
+  return p->I % 128 == 0 ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
 WsLayout ws_layout(const moe_problem_t& p) {
@@ -289,6 +297,53 @@ moe_status_t moe_expert_ffn_waved_fp8(const moe_problem_t* p, const uint8_t* x_f
   return hip_status(launch_ffn_fp8(*p, L, x_fp8, x_scale, packed, expert_offsets, sorted_token, pair_pos,
                                    topk_w, y, out, flags, static_cast<char*>(ws),
                                    static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_mxfp4_codes_stride(int32_t d) { return d > 0 && d % 128 == 0 ? mx_codes_stride(d) : 0; }
+size_t moe_mxfp4_scales_stride(int32_t d) { return d > 0 && d % 128 == 0 ? mx_scales_stride(d) : 0; }
+
+moe_status_t moe_quantize_mxfp4(const moe_problem_t* p, const void* x, uint8_t* codes, uint8_t* scales,
+                                moe_stream_t stream) {
+  moe_status_t st = check_problem(p);
+  if (st != MOE_OK) return st;
+  if (p->T > 0 && (!x || !codes || !scales)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_quantize_mxfp4(*p, x, codes, scales, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_dequantize_mxfp4(const moe_problem_t* p, const uint8_t* codes, const uint8_t* scales, void* x,
+                                  moe_stream_t stream) {
+  moe_status_t st = check_problem(p);
+  if (st != MOE_OK) return st;
+  if (p->T > 0 && (!x || !codes || !scales)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_dequantize_mxfp4(*p, codes, scales, x, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_packed_mxfp4_size(const moe_problem_t* p) {
+  if (check_mx(p) != MOE_OK) return 0;
+  return packed_mx_layout(p->d, p->I, p->E_global, p->E_local, p->x_dtype == MOE_BF16, gate_rows(*p)).total;
+}
+
+moe_status_t moe_pack_weights_mxfp4(const moe_problem_t* p, const void* Wg, const void* W1, const void* W3,
+                                    const void* W2, void* packed, moe_stream_t stream) {
+  moe_status_t st = check_mx(p);
+  if (st != MOE_OK) return st;
+  const bool need_w3 = p->activation == MOE_ACT_SWIGLU;
+  if (!Wg || !W1 || (need_w3 && !W3) || !W2 || !packed) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(packed) || !aligned16(Wg) || !aligned16(W1) || !aligned16(W3) || !aligned16(W2))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_pack_mxfp4(*p, Wg, W1, W3, W2, packed, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_unpack_weights_mxfp4(const moe_problem_t* p, const void* packed, void* W1, void* W3, void* W2,
+                                      moe_stream_t stream) {
+  moe_status_t st = check_mx(p);
+  if (st != MOE_OK) return st;
+  const bool gated = p->activation == MOE_ACT_SWIGLU;
+  if (!packed || !W1 || !W2 || (gated != (W3 != nullptr))) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(packed) || !aligned16(W1) || !aligned16(W3) || !aligned16(W2)) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_unpack_mxfp4(*p, packed, W1, W3, W2, static_cast<hipStream_t>(stream)));
 }
 
 moe_status_t moe_combine(const moe_problem_t* p, const void* y, const int32_t* pair_pos,

@@ -126,6 +126,8 @@ struct BackwardArgs {
 // Each returns hipSuccess or the launch error.  Shapes are validated by the
 // caller (moe_api.hip) before these run.
 
+// The router weights of either packed buffer (offset 0 of both).
+hipError_t launch_pack_router(const moe_problem_t& p, const void* Wg, void* dst, hipStream_t s);
 hipError_t launch_pack(const moe_problem_t& p, const void* Wg, const void* W1, const void* W3,
                        const void* W2, void* packed, hipStream_t s);
 hipError_t launch_pack_bwd(const moe_problem_t& p, const void* Wg, const void* W1, const void* W3,
@@ -199,6 +201,17 @@ hipError_t launch_ffn_fp8(const moe_problem_t& p, const WsLayout& L, const uint8
                           const void* packed, const int32_t* offsets, const int32_t* sorted_token,
                           const int32_t* pair_pos, const float* topk_w, void* y, void* out, uint32_t flags,
                           char* ws, hipStream_t s);
+
+// MXFP4: token rows to codes and scales and back; the expert weights to the
+// 4-bit packed buffer and back (mxfp4.h).
+hipError_t launch_quantize_mxfp4(const moe_problem_t& p, const void* x, uint8_t* codes, uint8_t* scales,
+                                 hipStream_t s);
+hipError_t launch_dequantize_mxfp4(const moe_problem_t& p, const uint8_t* codes, const uint8_t* scales, void* x,
+                                   hipStream_t s);
+hipError_t launch_pack_mxfp4(const moe_problem_t& p, const void* Wg, const void* W1, const void* W3, const void* W2,
+                             void* packed, hipStream_t s);
+hipError_t launch_unpack_mxfp4(const moe_problem_t& p, const void* packed, void* W1, void* W3, void* W2,
+                               hipStream_t s);
 
 hipError_t launch_combine(const moe_problem_t& p, const void* y, const int32_t* pair_pos,
                           const float* topk_w, void* out, hipStream_t s);

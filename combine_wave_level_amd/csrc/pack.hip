@@ -139,26 +139,29 @@ hipError_t launch_pack_bwd(const moe_problem_t& p, const void* Wg, const void* W
   return hipGetLastError();
 }
 
+hipError_t launch_pack_router(const moe_problem_t& p, const void* Wg, void* dst, hipStream_t s) {
+  const int threads = 256, Epad = static_cast<int>(align_up(static_cast<size_t>(p.E_global), 128));
+  if (p.x_dtype == MOE_BF16) {
+    const size_t slots = static_cast<size_t>(Epad) * (p.d / 8);
+    dim3 grid(static_cast<unsigned>((slots + threads - 1) / threads), 1);
+    pack_frag_kernel<true, 0><<<grid, threads, 0, s>>>(Wg, nullptr, static_cast<uint16_t*>(dst), p.d, Epad,
+                                                       p.E_global, 0, 0);
+  } else {
+    const size_t n = static_cast<size_t>(p.d) * Epad;
+    pack_router_f32_kernel<<<static_cast<unsigned>((n + threads - 1) / threads), threads, 0, s>>>(
+        static_cast<const float*>(Wg), static_cast<float*>(dst), p.d, p.E_global, Epad);
+  }
+  return hipGetLastError();
+}
+
 hipError_t launch_pack(const moe_problem_t& p, const void* Wg, const void* W1, const void* W3,
                        const void* W2, void* packed, hipStream_t s) {
-  const bool xbf = p.x_dtype == MOE_BF16;
   const bool wbf = p.w_dtype == MOE_BF16;
-  const PackedLayout L = packed_layout(p.d, p.I, p.E_global, p.E_local, xbf, gate_rows(p));
+  const PackedLayout L =
+      packed_layout(p.d, p.I, p.E_global, p.E_local, p.x_dtype == MOE_BF16, gate_rows(p));
   char* base = static_cast<char*>(packed);
   const int threads = 256;
-  // router
-  if (xbf) {
-    const size_t slots = static_cast<size_t>(L.Epad) * (p.d / 8);
-    dim3 grid(static_cast<unsigned>((slots + threads - 1) / threads), 1);
-    pack_frag_kernel<true, 0><<<grid, threads, 0, s>>>(Wg, nullptr,
-        reinterpret_cast<uint16_t*>(base + L.router), p.d, L.Epad, p.E_global, 0, 0);
-  } else {
-    const size_t n = static_cast<size_t>(p.d) * L.Epad;
-    pack_router_f32_kernel<<<static_cast<unsigned>((n + threads - 1) / threads), threads, 0, s>>>(
-        static_cast<const float*>(Wg), reinterpret_cast<float*>(base + L.router), p.d, p.E_global,
-        L.Epad);
-  }
-  hipError_t e = hipGetLastError();
+  hipError_t e = launch_pack_router(p, Wg, base + L.router, s);
   if (e != hipSuccess) return e;
   if (p.E_local == 0) return hipSuccess;
   if (p.activation != MOE_ACT_SWIGLU) {

@@ -37,6 +37,8 @@ EXPORTED = (
     "moe_packed_bwd_size", "moe_pack_weights_bwd", "moe_backward", "moe_quantize_fp8",
     "moe_expert_ffn_waved_fp8", "moe_ffn_path", "moe_route_noalloc", "moe_route_dispatch", "moe_probe_mfma",
     "moe_probe_copy", "moe_expert_ffn_waved_save_h", "moe_backward_saved_h", "moe_saved_h_bytes",
+    "moe_mxfp4_codes_stride", "moe_mxfp4_scales_stride", "moe_quantize_mxfp4", "moe_dequantize_mxfp4",
+    "moe_packed_mxfp4_size", "moe_pack_weights_mxfp4", "moe_unpack_weights_mxfp4",
     "moe_check_error", "moe_status_string", "moe_version",
 )
 
@@ -103,6 +105,13 @@ def lib() -> ctypes.CDLL:
             "moe_quantize_fp8": (st, [P, vp, vp, f32p, vp]),
             "moe_expert_ffn_waved_fp8": (st, [P, vp, f32p, vp, i32p, i32p, i32p, f32p, i32p, vp, vp,
                                               ctypes.c_uint32, vp, ctypes.c_size_t, vp]),
+            "moe_mxfp4_codes_stride": (ctypes.c_size_t, [ctypes.c_int32]),
+            "moe_mxfp4_scales_stride": (ctypes.c_size_t, [ctypes.c_int32]),
+            "moe_quantize_mxfp4": (st, [P, vp, vp, vp, vp]),
+            "moe_dequantize_mxfp4": (st, [P, vp, vp, vp, vp]),
+            "moe_packed_mxfp4_size": (ctypes.c_size_t, [P]),
+            "moe_pack_weights_mxfp4": (st, [P, vp, vp, vp, vp, vp, vp]),
+            "moe_unpack_weights_mxfp4": (st, [P, vp, vp, vp, vp, vp]),
             "moe_probe_mfma": (st, [f32p, ctypes.c_size_t, ctypes.c_int32, ctypes.POINTER(ctypes.c_double), vp]),
             "moe_probe_copy": (st, [vp, vp, ctypes.c_size_t, vp]),
             "moe_check_error": (st, [vp, vp]),
@@ -321,6 +330,96 @@ def ffn_waved_fp8(p: Problem, x8, x_scale, packed, disp: Dispatch, topk_w, ws, f
         _p(disp.pair_pos), _p(topk_w), _p(disp.ready_wave), _p(y), _p(out) if fused_combine else None,
         flags, _p(ws), ws.numel(), _stream()), "moe_expert_ffn_waved_fp8")
     return y, (out if fused_combine else None)
+
+
+_TORCH_DTYPE = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}
+
+
+def _need(name, t, shape, dtype):
+    """The library reads dense row-major memory of one type on the current
+    GPU: anything else is refused here, where the tensor still says what it is."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        got = f"{t.dtype} {tuple(t.shape)}" if isinstance(t, torch.Tensor) else type(t).__name__
+        raise ValueError(f"{name}: {dtype} of shape {tuple(shape)} expected, got {got}")
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, not on the current GPU")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous (strides {t.stride()})")
+
+
+def mxfp4_strides(d: int):
+    """Bytes per row of the codes and of the scales of d elements in MXFP4
+    (d % 128 == 0)."""
+    cs, ss = int(lib().moe_mxfp4_codes_stride(d)), int(lib().moe_mxfp4_scales_stride(d))
+    if cs == 0:
+        raise MoEError(MOE_ERR_UNSUPPORTED, "moe_mxfp4_codes_stride")
+    return cs, ss
+
+
+def quantize_mxfp4(p: Problem, x):
+    """MXFP4 codes (uint8 [T, codes stride], two to a byte) and scales (uint8
+    [T, scales stride], 2^(byte - 127) per 32 elements) of the rows of x
+    [T, d]; see moe_quantize_mxfp4 for the rule."""
+    _need("x", x, (p.T, p.d), _TORCH_DTYPE[p.x_dtype])
+    cs, ss = mxfp4_strides(p.d)
+    codes = torch.empty((p.T, cs), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((p.T, ss), dtype=torch.uint8, device=x.device)
+    _check(lib().moe_quantize_mxfp4(ctypes.byref(p), _p(x), _p(codes), _p(scales), _stream()), "moe_quantize_mxfp4")
+    return codes, scales
+
+
+def _need_mxfp4_rows(p: Problem, codes, scales):
+    cs, ss = mxfp4_strides(p.d)
+    _need("codes", codes, (p.T, cs), torch.uint8)
+    _need("scales", scales, (p.T, ss), torch.uint8)
+
+
+def dequantize_mxfp4(p: Problem, codes, scales):
+    """The rows codes and scales stand for: [T, d] in the problem's x dtype (exact)."""
+    _need_mxfp4_rows(p, codes, scales)
+    x = torch.empty((p.T, p.d), dtype=_TORCH_DTYPE[p.x_dtype], device=codes.device)
+    _check(lib().moe_dequantize_mxfp4(ctypes.byref(p), _p(codes), _p(scales), _p(x), _stream()),
+           "moe_dequantize_mxfp4")
+    return x
+
+
+def packed_mxfp4_size(p: Problem) -> int:
+    return int(lib().moe_packed_mxfp4_size(ctypes.byref(p)))
+
+
+def pack_weights_mxfp4(p: Problem, Wg, W1, W3, W2) -> torch.Tensor:
+    """The router weights and the experts' weights in MXFP4, packed for
+    ffn_mxfp4 and forward_few(mxfp4=True); also serves as `packed` of route
+    and route_dispatch.  W3 None for the ungated activation."""
+    n = packed_mxfp4_size(p)
+    if n == 0:
+        raise MoEError(MOE_ERR_UNSUPPORTED, "moe_packed_mxfp4_size")
+    wt = _TORCH_DTYPE[p.w_dtype]
+    _need("Wg", Wg, (p.d, p.E_global), _TORCH_DTYPE[p.x_dtype])
+    _need("W1", W1, (p.E_local, p.d, p.I), wt)
+    if p.activation == MOE_ACT_SWIGLU:
+        _need("W3", W3, (p.E_local, p.d, p.I), wt)
+    _need("W2", W2, (p.E_local, p.I, p.d), wt)
+    packed = torch.empty(n, dtype=torch.uint8, device=W1.device)
+    _check(lib().moe_pack_weights_mxfp4(ctypes.byref(p), _p(Wg), _p(W1), _p(W3), _p(W2), _p(packed), _stream()),
+           "moe_pack_weights_mxfp4")
+    return packed
+
+
+def unpack_weights_mxfp4(p: Problem, packed):
+    """W1, W3, W2 (W3 None for the ungated activation) that the packed experts
+    stand for, in math layout and the problem's w dtype (exact)."""
+    n = packed_mxfp4_size(p)
+    if n == 0:
+        raise MoEError(MOE_ERR_UNSUPPORTED, "moe_packed_mxfp4_size")
+    _need("packed", packed, (n,), torch.uint8)
+    wt, dev = _TORCH_DTYPE[p.w_dtype], packed.device
+    W1 = torch.empty((p.E_local, p.d, p.I), dtype=wt, device=dev)
+    W3 = torch.empty((p.E_local, p.d, p.I), dtype=wt, device=dev) if p.activation == MOE_ACT_SWIGLU else None
+    W2 = torch.empty((p.E_local, p.I, p.d), dtype=wt, device=dev)
+    _check(lib().moe_unpack_weights_mxfp4(ctypes.byref(p), _p(packed), _p(W1), _p(W3), _p(W2), _stream()),
+           "moe_unpack_weights_mxfp4")
+    return W1, W3, W2
 
 
 def combine(p: Problem, y, pair_pos, topk_w, out=None):

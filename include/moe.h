@@ -310,6 +310,57 @@ moe_status_t moe_expert_ffn_waved_fp8(const moe_problem_t* p, const uint8_t* x_f
                                       void* out, uint32_t flags, void* ws, size_t ws_bytes,
                                       moe_stream_t stream);
 
+/* ------------------------------------------------------------ MXFP4
+ * The 4-bit microscaled format: blocks of 32 consecutive elements with one
+ * scale 2^k (a byte, k + 127) and E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives), two to a byte, the even element in the low four bits.
+ * The library's quantisation of a block: k is the smallest integer >= -127
+ * with max |v| <= 6 * 2^k (no element saturates; the rule of
+ * moe_quantize_fp8), each code the E2M1 value nearest to v / 2^k, ties to
+ * the even code; a value that rounds to zero keeps its sign.  Values that
+ * already are MXFP4 values of their block stay what they are.  A block that
+ * holds an infinity or a NaN gets scale byte 255 and codes 0 and reads as NaN
+ * throughout.  (A value above 3.5 * 2^126 rounds to 4 * 2^126, which an fp32
+ * or bf16 reader sees as infinity.)  The caller may bring codes and scales of any other rule.
+ *
+ * Token rows of d elements: codes in moe_mxfp4_codes_stride(d) bytes a row
+ * (d / 2 rounded up to 128), scales in moe_mxfp4_scales_stride(d) bytes a row
+ * (d / 32 rounded up to 16); the padding is never used in a result.  0 for
+ * d <= 0 or d % 128 != 0. */
+size_t moe_mxfp4_codes_stride(int32_t d);
+size_t moe_mxfp4_scales_stride(int32_t d);
+
+/* x [T, d] in x_dtype -> codes [T, codes_stride], scales [T, scales_stride],
+ * written entirely (padding zero). */
+moe_status_t moe_quantize_mxfp4(const moe_problem_t* p, const void* x, uint8_t* codes, uint8_t* scales,
+                                moe_stream_t stream);
+
+/* The values codes and scales stand for: x [T, d] in x_dtype (exact in both
+ * types). */
+moe_status_t moe_dequantize_mxfp4(const moe_problem_t* p, const uint8_t* codes, const uint8_t* scales, void* x,
+                                  moe_stream_t stream);
+
+/* Bytes of the 4-bit weight buffer. 0 on a bad shape; the MXFP4 entry points
+ * below need I % 128 == 0 (MOE_ERR_UNSUPPORTED otherwise). */
+size_t moe_packed_mxfp4_size(const moe_problem_t* p);
+
+/* moe_pack_weights for the MXFP4 products: the expert weights quantised
+ * along each product's reduction index (d for W1 and W3, I for W2; from
+ * w_dtype, fp32 not rounded to bf16 first) into the layout of the 4-bit
+ * matrix instruction.  The router weights lie where moe_pack_weights puts
+ * them, so the buffer also serves moe_route, moe_route_dispatch and
+ * moe_route_noalloc.  Arguments as moe_pack_weights; packed:
+ * moe_packed_mxfp4_size(p) bytes. */
+moe_status_t moe_pack_weights_mxfp4(const moe_problem_t* p, const void* Wg, const void* W1, const void* W3,
+                                    const void* W2, void* packed, moe_stream_t stream);
+
+/* The values the packed experts stand for, in math layout and w_dtype (exact
+ * in both types): W1, W3 [E_local, d, I] (W3 NULL for RELU2, required for
+ * SWIGLU), W2 [E_local, I, d].  For a backward on the quantised weights
+ * (moe_pack_weights and moe_pack_weights_bwd of these), or an export. */
+moe_status_t moe_unpack_weights_mxfp4(const moe_problem_t* p, const void* packed, void* W1, void* W3, void* W2,
+                                      moe_stream_t stream);
+
 /* Combine (digest section 1.1; 10100.com deterministic operators): for each
  * token, out[t] = sum over ranks j = 0..k-1 with pair_pos[t, j] >= 0 of
  * topk_w[t, j] * y[pair_pos[t, j]], accumulated in fp32 with fused

@@ -19,4 +19,7 @@ from .moe_oracle import (  # noqa: F401
     e4m3_decode,
     e4m3_encode,
     quantize_fp8_per_token,
+    e2m1_decode,
+    e2m1_encode,
+    quantize_mxfp4,
 )

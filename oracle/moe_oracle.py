@@ -69,6 +69,9 @@ __all__ = [
     "e4m3_decode",
     "e4m3_encode",
     "quantize_fp8_per_token",
+    "e2m1_decode",
+    "e2m1_encode",
+    "quantize_mxfp4",
 ]
 
 
@@ -536,3 +539,52 @@ def quantize_fp8_per_token(x: np.ndarray):
     codes = e4m3_encode(x / scale[:, None])
     deq = e4m3_decode(codes) * scale[:, None]
     return codes, scale, deq
+
+
+# ---------------------------------------------------------------- MXFP4
+
+_E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def e2m1_encode(v: np.ndarray) -> np.ndarray:
+    """Nearest E2M1 code (sign bit 8) of float64 values with |v| <= 6, ties to
+    the even code, by distance to each of the eight magnitudes."""
+    v = np.asarray(v, dtype=np.float64)
+    if np.any(np.abs(v) > 6.0) or np.any(np.isnan(v)):
+        raise ValueError("e2m1_encode expects values with |v| <= 6")
+    a = np.abs(v)
+    best = np.zeros(a.shape, dtype=np.uint8)
+    dist = np.abs(a - _E2M1[0])
+    for c in range(1, 8):
+        dc = np.abs(a - _E2M1[c])
+        take = (dc < dist) | ((dc == dist) & (c % 2 == 0))
+        best = np.where(take, np.uint8(c), best)
+        dist = np.where(take, dc, dist)
+    return (best | np.where(np.signbit(v), 8, 0)).astype(np.uint8)
+
+
+def e2m1_decode(codes: np.ndarray) -> np.ndarray:
+    c = np.asarray(codes, dtype=np.uint8)
+    return np.where(c & 8, -1.0, 1.0) * _E2M1[c & 7]
+
+
+def quantize_mxfp4(v: np.ndarray):
+    """MXFP4 of float64 values, blocks of 32 along the last axis: scale 2^k,
+    k the smallest integer >= -127 with max |v| <= 6 * 2^k; a block with an
+    infinity or a NaN has scale byte 255 and codes 0.  Returns (codes uint8,
+    one an element, scale bytes uint8 [..., n / 32], values float64)."""
+    v = np.asarray(v, dtype=np.float64)
+    b = v.reshape(v.shape[:-1] + (-1, 32))
+    amax = np.abs(b).max(axis=-1)                    # NaN propagates
+    bad = ~np.isfinite(amax)
+    a = np.where(bad, 0.0, amax)
+    k = np.full(a.shape, -127, dtype=np.int64)
+    grow = a > 6.0 * np.exp2(k.astype(np.float64))
+    while np.any(grow):
+        k = np.where(grow, k + 1, k)
+        grow = a > 6.0 * np.exp2(k.astype(np.float64))
+    q = np.where(bad[..., None], 0.0, b) / np.exp2(k.astype(np.float64))[..., None]
+    codes = np.where(bad[..., None], np.uint8(0), e2m1_encode(q)).astype(np.uint8)
+    vals = e2m1_decode(codes) * np.exp2(k.astype(np.float64))[..., None]
+    vals = np.where(bad[..., None], np.nan, vals)
+    return codes.reshape(v.shape), np.where(bad, 255, k + 127).astype(np.uint8), vals.reshape(v.shape)

@@ -1,0 +1,166 @@
+"""MXFP4 conversions on the GPU, through the C ABI: codes, scales and values
+equal the float64 oracle's bit for bit (no rounding is left to tolerate: a
+code is a choice among eight values and a value times a power of two is
+exact)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from combine_wave_level_amd import moe
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": (moe.MOE_BF16, torch.bfloat16), "f32": (moe.MOE_F32, torch.float32)}
+
+
+def _problem(T=1, d=256, I=128, E=1, x="bf16", w="bf16", act=moe.MOE_ACT_SWIGLU):
+    return moe.problem(T=T, d=d, I=I, E_global=E, k=1, experts_per_wave=1, x_dtype=DT[x][0], w_dtype=DT[w][0],
+                       activation=act)
+
+
+def _unpack_codes(c, d):
+    return np.stack([c & 15, c >> 4], -1).reshape(c.shape[0], -1)[:, :d], c[:, d // 2:]
+
+
+def _same(a, b):
+    bad = np.argwhere(~((a == b) | (np.isnan(a) & np.isnan(b))))
+    for i in bad[:5]:
+        print("  differs at", tuple(i), a[tuple(i)], b[tuple(i)], flush=True)
+    return len(bad) == 0
+
+
+def _check_rows(x, dt):
+    """x: float32 array whose values the type holds."""
+    T, d = x.shape
+    p = _problem(T=T, d=d, x=dt)
+    xd = torch.from_numpy(x).cuda().to(DT[dt][1])
+    x64 = xd.cpu().float().numpy().astype(np.float64)
+    codes, scales = moe.quantize_mxfp4(p, xd)
+    back = moe.dequantize_mxfp4(p, codes, scales)
+    torch.cuda.synchronize()
+    assert back.dtype == xd.dtype
+    oc, osb, ov = oracle.quantize_mxfp4(x64)
+    got, pad = _unpack_codes(codes.cpu().numpy(), d)
+    sb = scales.cpu().numpy()
+    assert (sb[:, :d // 32] == osb).all() and (sb[:, d // 32:] == 0).all() and (pad == 0).all()
+    assert (got == oc).all()
+    # the value in the type: exact, but 4 * 2^126 = 2^128 (a block of fp32's
+    # last half binade rounds up to it) lies half a step above the largest
+    # fp32, 2^128 - 2^104, and is infinity there
+    with np.errstate(over="ignore"):
+        ov = ov.astype(np.float32).astype(np.float64)
+    assert _same(back.cpu().float().numpy().astype(np.float64), ov)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d", [(1, 128), (3, 256), (2, 384), (17, 640), (5, 1152), (301, 4096), (8, 7168)])
+def test_rows(T, d, dt):
+    print(f"[case] mxfp4 rows T={T} d={d} {dt}", flush=True)
+    rng = np.random.default_rng(T * d)
+    x = rng.standard_normal((T, d)) * np.exp2(rng.integers(-20, 20, (T, 1)))
+    _check_rows(x.astype(np.float32), dt)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_crafted_blocks(dt):
+    print(f"[case] mxfp4 crafted {dt}", flush=True)
+    mids = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    x = np.zeros((9, 256), dtype=np.float64)
+    x[0, :7], x[0, 8:15], x[0, 16] = mids, -mids, 6.0                       # ties
+    step = 2.0 ** (-7 if dt == "bf16" else -20)
+    x[0, 32:39], x[0, 40:47], x[0, 48] = mids * (1 + step), -mids * (1 - step), -6.0   # just past them
+    x[1, 0:32] = -1e-9                                                      # one value fills a block
+    x[1, 32], x[1, 33] = -6.0, -0.2                                         # rounds to -0
+    x[2, :3] = [6.0 * 2.0 ** 5, 1, 2]                                       # amax on the border
+    x[2, 32:35] = [6.0 * 2.0 ** 5 * (1 + 2.0 ** -7), 1, 2]                  # and just above
+    x[3, 0], x[3, 32], x[3, 64] = 2.0 ** -126, 2.0 ** -127, 1.5 * 2.0 ** -124   # the smallest scales
+    x[4, 0], x[4, 33] = np.float32(3.0e38), np.float32(-2.0e38)             # the largest
+    x[5, 5], x[5, 40], x[5, 70] = np.inf, -np.inf, np.nan                   # whole blocks read as NaN
+    x[5, 6] = 3.0
+    x[6] = np.linspace(-6, 6, 256)
+    x[7, 96:128] = np.arange(32) * 2.0 ** -120
+    _check_rows(x.astype(np.float32), dt)
+
+
+def test_no_rows():
+    p = _problem(T=0)
+    codes, scales = moe.quantize_mxfp4(p, torch.empty(0, 256, dtype=torch.bfloat16, device="cuda"))
+    assert moe.dequantize_mxfp4(p, codes, scales).shape == (0, 256)
+
+
+@pytest.mark.parametrize("E,d,I,w,act", [(1, 128, 128, "bf16", moe.MOE_ACT_SWIGLU), (3, 384, 256, "f32", moe.MOE_ACT_SWIGLU),
+                                         (2, 640, 384, "bf16", moe.MOE_ACT_RELU2), (2, 1152, 640, "f32", moe.MOE_ACT_RELU2),
+                                         (2, 512, 1024, "bf16", moe.MOE_ACT_SWIGLU)])
+def test_weights_round_trip(E, d, I, w, act):
+    """pack then unpack equals the oracle's values of blocks along d (W1, W3)
+    and along I (W2)."""
+    print(f"[case] mxfp4 weights E={E} d={d} I={I} {w} act={act}", flush=True)
+    g = torch.Generator().manual_seed(E * d + I)
+    mk = lambda *s: (torch.randn(*s, generator=g) * 0.02).to(DT[w][1])
+    W1, W2 = mk(E, d, I), mk(E, I, d)
+    W3 = mk(E, d, I) if act == moe.MOE_ACT_SWIGLU else None
+    W1[0, :32, 0] = 0
+    W1[E - 1, 5, I - 1] = float("nan")
+    p = _problem(d=d, I=I, E=E, w=w, act=act)
+    Wg = torch.zeros(d, E, dtype=torch.bfloat16, device="cuda")
+    D1, D3, D2 = W1.cuda(), None if W3 is None else W3.cuda(), W2.cuda()
+    packed = moe.pack_weights_mxfp4(p, Wg, D1, D3, D2)
+    # every byte is written: the same again over a poisoned buffer
+    again = torch.full_like(packed, 0xA5)
+    st = moe.lib().moe_pack_weights_mxfp4(ctypes.byref(p), moe._p(Wg), moe._p(D1), moe._p(D3), moe._p(D2),
+                                          moe._p(again), moe._stream())
+    assert st == moe.MOE_OK
+    got = moe.unpack_weights_mxfp4(p, packed)
+    torch.cuda.synchronize()
+    gr = 1 if W3 is None else 2
+    for off, n in _regions(p, gr):
+        assert torch.equal(packed[off:off + n], again[off:off + n])
+    for name, src, out in (("W1", W1, got[0]), ("W3", W3, got[1]), ("W2", W2, got[2])):
+        if src is None:
+            assert out is None
+            continue
+        assert out.dtype == src.dtype and out.shape == src.shape
+        want = oracle.quantize_mxfp4(np.swapaxes(src.double().numpy(), 1, 2))[2]
+        assert _same(np.swapaxes(out.float().cpu().numpy().astype(np.float64), 1, 2), want), name
+
+
+def _regions(p, gr):
+    """(offset, bytes) of the parts of the packed buffer."""
+    up = lambda n: -(-n // 1024) * 1024
+    off, out = 0, []
+    kq = lambda K: -(-K // 512)
+    for n in (128 * p.d * 2, p.E_local * gr * p.I * p.d // 2, p.E_local * (gr * p.I // 64) * kq(p.d) * 1024,
+              p.E_local * p.d * p.I // 2, p.E_local * (p.d // 64) * kq(p.I) * 1024):
+        out.append((off, n))
+        off += up(n)
+    assert off == moe.packed_mxfp4_size(p)
+    return out
+
+
+def test_the_packed_buffer_routes_like_the_bf16_one():
+    p = _problem(T=33, d=512, I=256, E=8)
+    p = p.replace(k=3)
+    g = torch.Generator().manual_seed(1)
+    mk = lambda *s: (torch.randn(*s, generator=g) * 0.02).bfloat16().cuda()
+    Wg, W1, W3, W2, x = mk(512, 8), mk(8, 512, 256), mk(8, 512, 256), mk(8, 256, 512), mk(33, 512)
+    ws = moe.workspace(p)
+    a = moe.route(p, x, moe.pack_weights(p, Wg, W1, W3, W2), ws, want_logits=True)
+    b = moe.route(p, x, moe.pack_weights_mxfp4(p, Wg, W1, W3, W2), ws, want_logits=True)
+    torch.cuda.synchronize()
+    for u, v in zip(a, b):
+        assert torch.equal(u, v)
+
+
+def test_refused_tensors():
+    p = _problem(T=4)
+    wide = torch.zeros(4, 512, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="not contiguous"):
+        moe.quantize_mxfp4(p, wide[:, :256])
+    with pytest.raises(ValueError, match="not contiguous"):
+        moe.quantize_mxfp4(p, torch.zeros(256, 4, dtype=torch.bfloat16, device="cuda").t())
+    # a row slice that starts off 16 bytes
+    with pytest.raises(moe.MoEError):
+        moe.quantize_mxfp4(p, torch.zeros(4 * 256 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(4, 256))
