@@ -346,6 +346,23 @@ moe_status_t moe_unpack_weights_mxfp4(const moe_problem_t* p, const void* packed
   return hip_status(launch_unpack_mxfp4(*p, packed, W1, W3, W2, static_cast<hipStream_t>(stream)));
 }
 
+moe_status_t moe_expert_ffn_mxfp4(const moe_problem_t* p, const uint8_t* codes, const uint8_t* scales,
+                                  const void* packed, const int32_t* expert_offsets, const int32_t* sorted_token,
+                                  const int32_t* pair_pos, const float* topk_w, void* y, void* out, void* ws,
+                                  size_t ws_bytes, moe_stream_t stream) {
+  moe_status_t st = check_mx(p);
+  if (st != MOE_OK) return st;
+  if (!packed || !expert_offsets) return MOE_ERR_INVALID_ARG;
+  if (p->T > 0 && (!codes || !scales || !sorted_token || !y)) return MOE_ERR_INVALID_ARG;
+  if (out && (!pair_pos || !topk_w)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(packed) || !aligned16(y) || !aligned16(out))
+    return MOE_ERR_INVALID_ARG;
+  WsLayout L;
+  if ((st = check_ws(p, ws, ws_bytes, &L)) != MOE_OK) return st;
+  return hip_status(launch_ffn_mxfp4(*p, L, codes, scales, packed, expert_offsets, sorted_token, pair_pos, topk_w, y,
+                                     out, static_cast<char*>(ws), static_cast<hipStream_t>(stream)));
+}
+
 moe_status_t moe_combine(const moe_problem_t* p, const void* y, const int32_t* pair_pos,
                          const float* topk_w, void* out, moe_stream_t stream) {
   moe_status_t st = check_problem(p);

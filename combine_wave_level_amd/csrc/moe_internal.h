@@ -213,6 +213,11 @@ hipError_t launch_pack_mxfp4(const moe_problem_t& p, const void* Wg, const void*
 hipError_t launch_unpack_mxfp4(const moe_problem_t& p, const void* packed, void* W1, void* W3, void* W2,
                                hipStream_t s);
 
+hipError_t launch_ffn_mxfp4(const moe_problem_t& p, const WsLayout& L, const uint8_t* xc, const uint8_t* xs,
+                            const void* packed, const int32_t* offsets, const int32_t* sorted_token,
+                            const int32_t* pair_pos, const float* topk_w, void* y, void* out, char* ws,
+                            hipStream_t s);
+
 hipError_t launch_combine(const moe_problem_t& p, const void* y, const int32_t* pair_pos,
                           const float* topk_w, void* out, hipStream_t s);
 

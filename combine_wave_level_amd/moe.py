@@ -8,6 +8,7 @@ is missing, loading fails loudly -- there is no fallback of any kind.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -39,6 +40,7 @@ EXPORTED = (
     "moe_probe_copy", "moe_expert_ffn_waved_save_h", "moe_backward_saved_h", "moe_saved_h_bytes",
     "moe_mxfp4_codes_stride", "moe_mxfp4_scales_stride", "moe_quantize_mxfp4", "moe_dequantize_mxfp4",
     "moe_packed_mxfp4_size", "moe_pack_weights_mxfp4", "moe_unpack_weights_mxfp4",
+    "moe_expert_ffn_mxfp4",
     "moe_check_error", "moe_status_string", "moe_version",
 )
 
@@ -112,6 +114,7 @@ def lib() -> ctypes.CDLL:
             "moe_packed_mxfp4_size": (ctypes.c_size_t, [P]),
             "moe_pack_weights_mxfp4": (st, [P, vp, vp, vp, vp, vp, vp]),
             "moe_unpack_weights_mxfp4": (st, [P, vp, vp, vp, vp, vp]),
+            "moe_expert_ffn_mxfp4": (st, [P, vp, vp, vp, i32p, i32p, i32p, f32p, vp, vp, vp, ctypes.c_size_t, vp]),
             "moe_probe_mfma": (st, [f32p, ctypes.c_size_t, ctypes.c_int32, ctypes.POINTER(ctypes.c_double), vp]),
             "moe_probe_copy": (st, [vp, vp, ctypes.c_size_t, vp]),
             "moe_check_error": (st, [vp, vp]),
@@ -347,6 +350,7 @@ def _need(name, t, shape, dtype):
         raise ValueError(f"{name}: not contiguous (strides {t.stride()})")
 
 
+@functools.lru_cache(maxsize=None)
 def mxfp4_strides(d: int):
     """Bytes per row of the codes and of the scales of d elements in MXFP4
     (d % 128 == 0)."""
@@ -420,6 +424,55 @@ def unpack_weights_mxfp4(p: Problem, packed):
     _check(lib().moe_unpack_weights_mxfp4(ctypes.byref(p), _p(packed), _p(W1), _p(W3), _p(W2), _stream()),
            "moe_unpack_weights_mxfp4")
     return W1, W3, W2
+
+
+def _need_dispatch(p: Problem, disp: Dispatch, topk_w):
+    i32 = torch.int32
+    _need("disp.offsets", disp.offsets, (p.E_local + 1,), i32)
+    _need("disp.sorted_token", disp.sorted_token, (max(1, p_max(p)),), i32)
+    _need("disp.pair_pos", disp.pair_pos, (p.T, p.k), i32)
+    _need("topk_w", topk_w, (p.T, p.k), torch.float32)
+
+
+def _need_workspace(p: Problem, ws):
+    # any size at least the forward one: the library checks the size itself
+    if not isinstance(ws, torch.Tensor):
+        raise ValueError("ws: a tensor from workspace() expected")
+    _need("ws", ws, ws.shape[:1], torch.uint8)
+
+
+def ffn_mxfp4(p: Problem, codes, scales, packed, disp: Dispatch, topk_w, ws, fused_combine=True, y=None, out=None):
+    """The expert FFN with both operands of both products in MXFP4: codes and
+    scales from quantize_mxfp4, packed from pack_weights_mxfp4.  Returns (y,
+    out) as ffn_waved."""
+    _need_mxfp4_rows(p, codes, scales)
+    _need("packed", packed, (packed_mxfp4_size(p),), torch.uint8)
+    _need_dispatch(p, disp, topk_w)
+    _need_workspace(p, ws)
+    dev = codes.device
+    if y is None:
+        y = torch.empty((max(1, p_max(p)), p.d), dtype=torch.bfloat16, device=dev)
+    else:
+        _need("y", y, (max(1, p_max(p)), p.d), torch.bfloat16)
+    if not fused_combine:
+        out = None
+    elif out is None:
+        out = torch.empty((p.T, p.d), dtype=_out_dtype(p), device=dev)
+    else:
+        _need("out", out, (p.T, p.d), _out_dtype(p))
+    _check(lib().moe_expert_ffn_mxfp4(
+        ctypes.byref(p), _p(codes), _p(scales), _p(packed), _p(disp.offsets), _p(disp.sorted_token),
+        _p(disp.pair_pos), _p(topk_w), _p(y), _p(out), _p(ws), ws.numel(), _stream()), "moe_expert_ffn_mxfp4")
+    return y, out
+
+
+def forward_mxfp4(p: Problem, x, packed, ws, bias=None, want_logits=False):
+    """The layer with MXFP4 experts: route and dispatch on x, MXFP4 rows of x,
+    expert FFN with the combine (packed from pack_weights_mxfp4)."""
+    idx, w, logits, disp = route_dispatch(p, x, packed, ws, bias=bias, want_logits=want_logits)
+    codes, scales = quantize_mxfp4(p, x)
+    y, out = ffn_mxfp4(p, codes, scales, packed, disp, w, ws)
+    return {"idx": idx, "w": w, "logits": logits, "disp": disp, "y": y, "out": out}
 
 
 def combine(p: Problem, y, pair_pos, topk_w, out=None):

@@ -361,6 +361,23 @@ moe_status_t moe_pack_weights_mxfp4(const moe_problem_t* p, const void* Wg, cons
 moe_status_t moe_unpack_weights_mxfp4(const moe_problem_t* p, const void* packed, void* W1, void* W3, void* W2,
                                       moe_stream_t stream);
 
+/* The expert FFN with both operands of both products in MXFP4: per routed
+ * pair, with xq the values of codes and scales and W1q, W3q, W2q those of the
+ * packed experts,
+ *   h1 = xq W1q, h3 = xq W3q, a = silu(h1) * h3 (RELU2: max(h1, 0)^2) in fp32,
+ *   y = MXFP4(a) W2q, a quantised by moe_quantize_mxfp4's rule along I;
+ * products accumulate in fp32 over K in one fixed ascending order, never
+ * split; y is rounded to bf16 and combined as moe_combine does.
+ *   codes, scales: from moe_quantize_mxfp4 (or the caller), row strides as
+ *   there.  packed: from moe_pack_weights_mxfp4.  The rest as
+ *   moe_expert_ffn_waved (same workspace after moe_dispatch).  The call runs
+ *   the phase schedule and may be repeated on one dispatch; calls that
+ *   overlap on one workspace race. */
+moe_status_t moe_expert_ffn_mxfp4(const moe_problem_t* p, const uint8_t* codes, const uint8_t* scales,
+                                  const void* packed, const int32_t* expert_offsets, const int32_t* sorted_token,
+                                  const int32_t* pair_pos, const float* topk_w, void* y, void* out, void* ws,
+                                  size_t ws_bytes, moe_stream_t stream);
+
 /* Combine (digest section 1.1; 10100.com deterministic operators): for each
  * token, out[t] = sum over ranks j = 0..k-1 with pair_pos[t, j] >= 0 of
  * topk_w[t, j] * y[pair_pos[t, j]], accumulated in fp32 with fused

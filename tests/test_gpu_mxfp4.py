@@ -164,3 +164,120 @@ def test_refused_tensors():
     # a row slice that starts off 16 bytes
     with pytest.raises(moe.MoEError):
         moe.quantize_mxfp4(p, torch.zeros(4 * 256 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(4, 256))
+
+
+# ------------------------------------------------------------------ the expert FFN
+
+def _layer(T, d, I, E, k, E_local=None, x="bf16", act=moe.MOE_ACT_SWIGLU, out=moe.MOE_BF16, seed=0, e_begin=0):
+    """Seeded weights and rows on the device, packed, with the float64 values
+    that the 4-bit operands stand for."""
+    E_local = E if E_local is None else E_local
+    g = torch.Generator().manual_seed(seed)
+    p = moe.problem(T=T, d=d, I=I, E_global=E, k=k, E_local=E_local, e_begin=e_begin, experts_per_wave=1,
+                    x_dtype=DT[x][0], out_dtype=out, activation=act)
+    mk = lambda *s: (torch.randn(*s, generator=g) * 0.02).bfloat16()
+    W1, W2 = mk(E_local, d, I), mk(E_local, I, d)
+    W3 = mk(E_local, d, I) if act == moe.MOE_ACT_SWIGLU else None
+    Wg = (torch.randn(d, E, generator=g) * 0.02).to(DT[x][1])
+    xr = torch.randn(T, d, generator=g).to(DT[x][1])
+    L = dict(p=p, W1=W1, W3=W3, W2=W2, Wg=Wg.cuda(), x=xr.cuda(), g=g, xr=xr)
+    L["packed"] = moe.pack_weights_mxfp4(p, L["Wg"], W1.cuda(), None if W3 is None else W3.cuda(), W2.cuda())
+    L["ws"] = moe.workspace(p)
+    return L
+
+
+def _grid(a, axis=-1):
+    a = np.swapaxes(a.double().numpy() if isinstance(a, torch.Tensor) else a, axis, -1)
+    return np.swapaxes(oracle.quantize_mxfp4(a)[2], axis, -1)
+
+
+def _routing(L, idx, w):
+    """Dispatch and MXFP4 rows of a routing given on the host."""
+    idx_d = torch.as_tensor(idx, dtype=torch.int32).cuda()
+    w_d = torch.as_tensor(w, dtype=torch.float32).cuda()
+    disp = moe.dispatch(L["p"], idx_d, L["ws"])
+    return disp, w_d
+
+
+def _reference(L, idx, w, toks):
+    """out of tokens toks in float64, a quantised in float64; and a bound of
+    what a flipped code of a can change.
+
+    The kernel's a differs from the float64 one by fp32 rounding, so an
+    element next to a rounding border (or a block next to a scale border) can
+    land on the other side: its value then moves by one code step, at most a
+    third of itself plus a quarter of the block's scale.  `flip` is what one
+    flip of the largest element of each row times its largest weight can move
+    an output by."""
+    p = L["p"]
+    x = _grid(L["xr"][toks])
+    W1, W2 = _grid(L["W1"], 1), _grid(L["W2"], 1)
+    W3 = None if L["W3"] is None else _grid(L["W3"], 1)
+    out = np.zeros((len(toks), p.d))
+    flip = np.zeros(len(toks))
+    for i, t in enumerate(toks):
+        for j in range(p.k):
+            e = int(idx[t, j]) - p.e_begin
+            if not 0 <= e < p.E_local:
+                continue
+            h1 = x[i] @ W1[e]
+            a = np.maximum(h1, 0) ** 2 if W3 is None else h1 / (1 + np.exp(-h1)) * (x[i] @ W3[e])
+            aq = _grid(a)
+            out[i] += w[t, j] * (aq @ W2[e])
+            flip[i] += w[t, j] * np.abs(aq).max() / 3 * np.abs(W2[e]).max()
+    return out, flip
+
+
+def _check_out(L, idx, w, out, toks):
+    """|out - ref| per element: y's rounding to bf16 (2^-8 of each |y|, so at
+    most 2^-8 of sum_j w_j |y_j|), out's own (2^-8 of |out|), fp32 sums (far
+    below), and at most two flipped codes of a row."""
+    ref, flip = _reference(L, idx, w, toks)
+    got = out[toks].float().cpu().numpy().astype(np.float64)
+    tol = 2.0 ** -7 * np.abs(ref).max(1) * 1.5 + 2 * flip
+    err = np.abs(got - ref).max(1)
+    print(f"  max err {err.max():.3g} of {np.abs(ref).max():.3g}; rms {np.sqrt(((got - ref) ** 2).mean()):.3g} "
+          f"of {np.sqrt((ref ** 2).mean()):.3g}", flush=True)
+    assert (err <= tol).all(), (err - tol).max()
+    # flips are rare: over all tokens the error is that of the two bf16 roundings
+    assert np.sqrt(((got - ref) ** 2).mean()) <= 2.0 ** -8 * 2 * np.sqrt((ref ** 2).mean()) + 1e-30
+
+
+def _random_routing(L, seed=1, skew=None):
+    p = L["p"]
+    rng = np.random.default_rng(seed)
+    score = rng.random((p.T, p.E_global))
+    if skew is not None:
+        score += skew
+    idx = np.argsort(-score, 1)[:, :p.k].astype(np.int32)
+    w = rng.random((p.T, p.k)) + 0.1
+    return idx, (w / w.sum(1, keepdims=True)).astype(np.float32)
+
+
+FFN = [  # T, d, I, E, k, E_local, x, act
+    (1, 128, 128, 1, 1, 1, "bf16", 0), (1, 256, 128, 4, 2, 4, "f32", 0), (5, 384, 256, 4, 3, 4, "bf16", 1),
+    (16, 640, 384, 5, 5, 5, "bf16", 0), (37, 1152, 640, 12, 3, 12, "f32", 1), (64, 512, 512, 1, 1, 1, "bf16", 0),
+    (65, 512, 256, 2, 2, 2, "bf16", 0),
+    (200, 256, 256, 2, 1, 2, "bf16", 0),      # the wide tiles from here: 256 by 256
+    (257, 384, 384, 2, 2, 2, "bf16", 1),      # 128 by 256, odd numbers of K steps
+    (300, 128, 128, 1, 1, 1, "bf16", 0),      # a single K step
+    (600, 640, 128, 3, 2, 3, "f32", 0),
+    (513, 896, 640, 4, 4, 2, "bf16", 0),      # a share
+    (1100, 1024, 512, 4, 2, 4, "bf16", 0),
+]
+
+
+@pytest.mark.parametrize("T,d,I,E,k,E_local,x,act", FFN)
+def test_ffn_against_float64(T, d, I, E, k, E_local, x, act):
+    print(f"[case] mxfp4 ffn T={T} d={d} I={I} E={E}/{E_local} k={k} {x} act={act}", flush=True)
+    L = _layer(T, d, I, E, k, E_local, x, act, seed=T + d)
+    idx, w = _random_routing(L)
+    disp, w_d = _routing(L, idx, w)
+    codes, scales = moe.quantize_mxfp4(L["p"], L["x"])
+    y, out = moe.ffn_mxfp4(L["p"], codes, scales, L["packed"], disp, w_d, L["ws"])
+    torch.cuda.synchronize()
+    moe.check_error(L["ws"])
+    toks = np.arange(T) if T <= 64 else np.unique(np.r_[0, T - 1, np.random.default_rng(0).choice(T, 40)])
+    _check_out(L, idx, w, out, toks)
+    # the standalone combine of the same y
+    assert torch.equal(moe.combine(L["p"], y, disp.pair_pos, w_d), out)
