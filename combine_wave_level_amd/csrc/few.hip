@@ -1,0 +1,511 @@
+// few.hip -- the whole layer for a few tokens (T <= 16): router, top-k, both
+// expert products and the combine, without dispatch tables.
+//
+// At most 16 tokens means at most 16 rows an expert: one 16-column block of
+// the matrix instruction.  The layer is then a stream of the touched
+// experts' weights, each fragment used once, so it goes from memory straight
+// into the operand registers of the wavefront that multiplies it (no LDS
+// stage: nothing would be shared), with the loads of the next fragments in
+// flight.  The tokens' operands are laid out k-major (16-byte pieces of one
+// k-group of all rows side by side), so that one matrix instruction's operand
+// is at most 1 KiB of consecutive memory, from the caches.
+//
+// Results are those of the composed path bit for bit (moe_route_dispatch,
+// then moe_expert_ffn_waved or moe_quantize_mxfp4 and moe_expert_ffn_mxfp4):
+// the same matrix instruction over the same unsplit ascending K for every
+// output element, the same partial sums of the router, the same selection
+// order, activation, roundings and combine order.
+#include "ffn_parts.h"
+#include "moe_internal.h"
+#include "mxfp4.h"
+#include "route_topk.h"
+
+namespace moe {
+namespace {
+
+constexpr int kFew = MOE_FEW_MAX_TOKENS;
+static_assert(kFew == 16, "one column block of the matrix instruction");
+constexpr int kMaxE = 256, kMaxK = 64;
+
+struct FewArgs {
+  const void* x;
+  const void* wg;          // router weights (packed buffer, offset 0)
+  const float* bias;
+  const uint8_t* w13;      // codes (bf16 or MXFP4 fragments) and MXFP4 scales
+  const uint8_t* w13s;
+  const uint8_t* w2;
+  const uint8_t* w2s;
+  float* partial;          // [splits][T][E]
+  uint8_t* xs;             // staged token operand, k-major; MXFP4: codes, then scales
+  uint8_t* act;            // activations, per slot k-major; MXFP4: codes, then scales
+  int32_t* topk_idx;
+  float* topk_w;
+  float* logits;
+  void* out;
+  int T, d, I, E, k, e_begin, E_local, splits;
+};
+
+// ------------------------------------------------------------------ kernel 1
+
+// Partial logits of 16 experts over one range of d by one wavefront: the
+// chain of matrix instructions of router_logits_mfma_kernel.
+__device__ __forceinline__ void few_logits_bf16(const FewArgs& A, int job) {
+  const int lane = lane_id(), r = lane & 15, g = lane >> 4;
+  const int neb = (A.E + 15) / 16, eb = job % neb, sp = job / neb;
+  const int ks = A.d / A.splits / 32, kb0 = sp * ks;
+  const uint16_t* w = static_cast<const uint16_t*>(A.wg) + frag_offset(eb, kb0, A.d / 32) + lane * 8;
+  const uint16_t* xr = static_cast<const uint16_t*>(A.x) + static_cast<size_t>(min(r, A.T - 1)) * A.d + kb0 * 32 + g * 8;
+  f32x4 acc{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int i = 0; i < ks; ++i) acc = mfma16x16x32(ld16(w + i * 512), ld16(xr + i * 32), acc);
+  if (r < A.T) {
+    float* o = A.partial + (static_cast<size_t>(sp) * A.T + r) * A.E;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (eb * 16 + 4 * g + i < A.E) o[eb * 16 + 4 * g + i] = acc[i];
+  }
+}
+
+// fp32 logits of 16 experts for all tokens by one workgroup: thread (t, e)
+// runs router_logits_f32_kernel's chain of fused multiply-adds over the
+// hidden index, both operands staged through LDS 128 indices at a time.
+__device__ __forceinline__ void few_logits_f32(const FewArgs& A, int eb, float* lds) {
+  const int Epad = static_cast<int>(align_up(static_cast<size_t>(A.E), 128));
+  const float *x = static_cast<const float*>(A.x), *wg = static_cast<const float*>(A.wg);
+  const int t = threadIdx.x / 16, e = threadIdx.x % 16;
+  float* sx = lds;              // [16][128]
+  float* sw = lds + 16 * 128;   // [128][16]
+  float nx[8], nw[8], acc = 0.f;
+  auto fetch = [&](int k0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int j = i * 256 + threadIdx.x;
+      nx[i] = j / 128 < A.T ? x[static_cast<size_t>(j / 128) * A.d + k0 + j % 128] : 0.f;
+      nw[i] = wg[static_cast<size_t>(k0 + j / 16) * Epad + eb * 16 + j % 16];
+    }
+  };
+  fetch(0);
+  for (int k0 = 0; k0 < A.d; k0 += 128) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      sx[i * 256 + threadIdx.x] = nx[i];
+      sw[i * 256 + threadIdx.x] = nw[i];
+    }
+    __syncthreads();
+    if (k0 + 128 < A.d) fetch(k0 + 128);
+#pragma unroll 16
+    for (int i = 0; i < 128; ++i) acc = fmaf(sx[t * 128 + i], sw[i * 16 + e], acc);
+  }
+  if (t < A.T && eb * 16 + e < A.E) A.partial[static_cast<size_t>(t) * A.E + eb * 16 + e] = acc;
+}
+
+// Stages eight elements of a token's row: bf16 (rounded from fp32), or codes
+// and scale (the quantiser's arithmetic; four lanes share a block).
+template <bool XBF, bool MX>
+__device__ __forceinline__ void few_stage(const FewArgs& A, int i) {
+  const int cpr = A.d / 8;
+  if (i >= A.T * cpr) return;  // cpr % 4 == 0: the lanes of a block leave together
+  const int t = i / cpr, c = i % cpr;
+  float v[8];
+  u32x4 raw{};
+  if constexpr (XBF) {
+    raw = ld16(static_cast<const uint16_t*>(A.x) + static_cast<size_t>(i) * 8);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(raw[j] << 16);
+      v[2 * j + 1] = __uint_as_float(raw[j] & 0xffff0000u);
+    }
+  } else {
+    const float* p = static_cast<const float*>(A.x) + static_cast<size_t>(i) * 8;
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = a[j];
+      v[4 + j] = b[j];
+    }
+  }
+  if constexpr (!MX) {
+    if constexpr (!XBF) raw = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    st16(A.xs + (static_cast<size_t>(c) * A.T + t) * 16, raw);
+  } else {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+    m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 1, kWave)));
+    m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 2, kWave)));
+    const uint32_t sb = mx_scale_byte(m);
+    const float inv = mx_inv_scale(sb);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = mx_scaled(v[j], inv, sb);
+    const int blk = c / 4;
+    *reinterpret_cast<uint32_t*>(A.xs + (static_cast<size_t>(blk) * A.T + t) * 16 + (c % 4) * 4) = mx_codes8(v);
+    if (c % 4 == 0) A.xs[static_cast<size_t>(A.T) * A.d / 2 + static_cast<size_t>(blk) * A.T + t] = static_cast<uint8_t>(sb);
+  }
+}
+
+// Logits and staged rows.  Workgroups [0, nlog): logits; the rest stage.
+template <bool XBF, bool MX>
+__global__ __launch_bounds__(256) void few_front_kernel(FewArgs A, int nlog) {
+  __shared__ float lds[XBF ? 1 : 4096];
+  const int b = blockIdx.x;
+  if (b < nlog) {
+    if constexpr (XBF) {
+      const int job = b * 4 + wave_id();
+      if (job < (A.E + 15) / 16 * A.splits) few_logits_bf16(A, job);
+    } else {
+      few_logits_f32(A, b, lds);
+    }
+    return;
+  }
+  few_stage<XBF, MX>(A, (b - nlog) * 256 + static_cast<int>(threadIdx.x));
+}
+
+// ------------------------------------------------------------------ routing in LDS
+
+// What every workgroup of the expert kernels derives from the partial logits
+// for itself (a few microseconds less than another kernel): the picks, their
+// weights, and the touched local experts ("slots") with their rows.
+struct FewRoute {
+  union {
+    float logit[kFew * kMaxE];
+    uint16_t y[kFew * kMaxK * 16];  // later: the pairs' outputs for 16 columns
+  };
+  int32_t idx[kFew * kMaxK];
+  float val[kFew * kMaxK];     // logit, then weight
+  float ex[kFew * kMaxK];
+  int16_t row[kFew * kMaxK];   // pair -> pair row, -1: expert not local
+  uint32_t mask[kMaxE];        // per local expert: the tokens that pick it
+  int16_t slot_of[kMaxE];
+  int16_t slot_e[kMaxE];       // slot -> local expert
+  int16_t base[kMaxE + 1];     // slot -> first pair row
+  int nslots;
+};
+
+__device__ __forceinline__ void few_route(const FewArgs& A, FewRoute& R, int nthreads, bool write) {
+  const int tid = threadIdx.x, TE = A.T * A.E, TK = A.T * A.k;
+  for (int i = tid; i < TE; i += nthreads) {
+    float acc = A.partial[i];
+    for (int sp = 1; sp < A.splits; ++sp) acc += A.partial[static_cast<size_t>(sp) * TE + i];
+    if (A.bias) acc += A.bias[i % A.E];
+    R.logit[i] = acc;
+    if (write && A.logits) A.logits[i] = acc;
+  }
+  // a token without enough comparable logits (NaN) picks no expert there, as
+  // topk_token leaves it
+  for (int i = tid; i < TK; i += nthreads) {
+    R.idx[i] = 0x7fffffff;
+    R.val[i] = -__builtin_inff();
+  }
+  for (int i = tid; i < kMaxE; i += nthreads) R.mask[i] = 0;
+  __syncthreads();
+  // rank of each expert by counting the better ones (NaN is never better)
+  for (int i = tid; i < TE; i += nthreads) {
+    const int t = i / A.E, e = i % A.E;
+    const float v = R.logit[i];
+    const float* row = R.logit + t * A.E;
+    int rank = 0;
+    for (int o = 0; o < A.E; ++o) rank += topk_better(row[o], o, v, e) ? 1 : 0;
+    if (v == v && rank < A.k) {
+      R.idx[t * A.k + rank] = e;
+      R.val[t * A.k + rank] = v;
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < TK; i += nthreads) {
+    const int t = i / A.k, le = R.idx[i] - A.e_begin;
+    R.ex[i] = expf(R.val[i] - R.val[t * A.k]);
+    if (le >= 0 && le < A.E_local) atomicOr(&R.mask[le], 1u << t);
+  }
+  __syncthreads();
+  for (int i = tid; i < TK; i += nthreads) {
+    const float* ex = R.ex + i / A.k * A.k;
+    float sum = 0.f;
+    for (int j = 0; j < A.k; ++j) sum += ex[j];  // ascending rank order
+    const float w = R.ex[i] / sum;
+    R.val[i] = w;
+    if (write) {
+      A.topk_idx[i] = R.idx[i];
+      A.topk_w[i] = w;
+    }
+  }
+  if (wave_id() == 0) {
+    const int lane = lane_id();
+    int slots = 0, rows = 0;
+#pragma unroll
+    for (int c = 0; c < kMaxE / kWave; ++c) {
+      const int e = c * kWave + lane, n = __popc(R.mask[e]);
+      int incl = n;
+#pragma unroll
+      for (int off = 1; off < kWave; off <<= 1) {
+        const int o = __shfl_up(incl, off, kWave);
+        incl += lane >= off ? o : 0;
+      }
+      const unsigned long long any = __ballot(n > 0);
+      const int s = slots + __popcll(any & ((1ull << lane) - 1));
+      if (n > 0) {
+        R.slot_e[s] = static_cast<int16_t>(e);
+        R.slot_of[e] = static_cast<int16_t>(s);
+        R.base[s] = static_cast<int16_t>(rows + incl - n);
+      }
+      slots += __popcll(any);
+      rows += __shfl(incl, kWave - 1, kWave);
+    }
+    if (lane == 0) {
+      R.base[slots] = static_cast<int16_t>(rows);
+      R.nslots = slots;
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < TK; i += nthreads) {
+    const int t = i / A.k, le = R.idx[i] - A.e_begin;
+    R.row[i] = le >= 0 && le < A.E_local
+                   ? static_cast<int16_t>(R.base[R.slot_of[le]] + __popc(R.mask[le] & ((1u << t) - 1)))
+                   : static_cast<int16_t>(-1);
+  }
+  __syncthreads();
+}
+
+// Token of row r of a slot's mask (r < popcount).
+__device__ __forceinline__ int nth_bit(uint32_t mask, int r) {
+  for (int i = 0; i < r; ++i) mask &= mask - 1;
+  return __ffs(mask) - 1;
+}
+
+// ------------------------------------------------------------------ the stream
+
+// One wavefront: 16 weight rows times the slot's tokens over the whole K.
+// w: the row block's fragments for this lane (1 KiB apart); b: this lane's
+// piece of the token operand, bstep bytes apart (a row past the slot's rows
+// repeats a valid one: its column is not used); MX: ws, bs the scale bytes,
+// 256 and bsstep bytes apart.  U fragments are in flight.
+template <bool MX, int U>
+__device__ __forceinline__ f32x4 few_stream(const uint8_t* __restrict__ w, const uint8_t* __restrict__ b, size_t bstep,
+                                            const uint8_t* __restrict__ ws, const uint8_t* __restrict__ bs,
+                                            size_t bsstep, int n) {
+  u32x4 ra[U], rb[U];
+  uint32_t sa[U], sb[U];
+  auto load = [&](int u, int i) {
+    i = min(i, n - 1);
+    ra[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w + static_cast<size_t>(i) * 1024));
+    rb[u] = ld16(b + static_cast<size_t>(i) * bstep);
+    if constexpr (MX) {
+      sa[u] = ws[static_cast<size_t>(i) * 256];
+      sb[u] = bs[static_cast<size_t>(i) * bsstep];
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(u, u);
+  f32x4 acc{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < n; i += U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i + u < n) {
+        if constexpr (MX) acc = mfma_mx<0, 0>(ra[u], rb[u], acc, sa[u], sb[u]);
+        else acc = mfma16x16x32(ra[u], rb[u], acc);
+      }
+      load(u, i + u + U);
+    }
+  }
+  return acc;
+}
+
+constexpr int kHStride = 17;  // floats per row of the h exchange
+
+// GEMM1 task: 64 packed rows (32 intermediate indices gated, 64 ungated) of
+// one slot, 16 rows a wavefront; gate and up meet in LDS, and 16 consecutive
+// lanes hold one token's block of 32 for the activation's scale.
+template <bool MX, bool GATED>
+__device__ __forceinline__ void few_gemm1(const FewArgs& A, const FewRoute& R, float* h, int slot, int nq) {
+  const int lane = lane_id(), r = lane & 15, g = lane >> 4;
+  const int e = R.slot_e[slot], base = R.base[slot], m = R.base[slot + 1] - base;
+  const uint32_t mask = R.mask[e];
+  const int N = (GATED ? 2 : 1) * A.I, tok = nth_bit(mask, min(r, m - 1));
+  const int nb = nq * 4 + wave_id();
+  f32x4 acc;
+  if constexpr (MX) {
+    const int KB = A.d / 128;
+    const uint8_t* w = A.w13 + e * mx_mat_codes(N, A.d) + static_cast<size_t>(nb) * KB * 1024 + lane * 16;
+    const uint8_t* ws = A.w13s + e * mx_mat_scales(N, A.d) + static_cast<size_t>(nq) * mx_kq(A.d) * 1024 + lane * 4 + wave_id();
+    const uint8_t* b = A.xs + (static_cast<size_t>(g) * A.T + tok) * 16;
+    const uint8_t* bs = A.xs + static_cast<size_t>(A.T) * A.d / 2 + static_cast<size_t>(g) * A.T + tok;
+    acc = few_stream<true, 8>(w, b, 64 * A.T, ws, bs, 4 * A.T, KB);
+  } else {
+    const int KB = A.d / 32;
+    const uint8_t* w = A.w13 + (static_cast<size_t>(e) * N * A.d + frag_offset(nb, 0, KB)) * 2 + lane * 16;
+    acc = few_stream<false, 8>(w, A.xs + (static_cast<size_t>(g) * A.T + tok) * 16, 64 * A.T, nullptr, nullptr, 0, KB);
+  }
+  __syncthreads();  // h free
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[(wave_id() * 16 + 4 * g + i) * kHStride + r] = acc[i];
+  __syncthreads();
+  const int t = threadIdx.x / 16, p = threadIdx.x % 16;  // row of the slot, element pair of a block
+  constexpr int NBLK = GATED ? 1 : 2;
+#pragma unroll
+  for (int blk = 0; blk < NBLK; ++blk) {
+    float v[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int q = 2 * p + i;  // element of the block
+      if constexpr (GATED) {
+        const int hr = (q / 16) * 32 + q % 16;
+        v[i] = silu_mul(h[hr * kHStride + t], h[(hr + 16) * kHStride + t]);
+      } else {
+        v[i] = relu_sq(h[(blk * 32 + q) * kHStride + t]);
+      }
+    }
+    const int kb = nq * NBLK + blk;  // block of 32 along I
+    if constexpr (MX) {
+      uint32_t mb = max(__float_as_uint(v[0]) & 0x7fffffffu, __float_as_uint(v[1]) & 0x7fffffffu);
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) mb = max(mb, static_cast<uint32_t>(__shfl_xor(static_cast<int>(mb), o, kWave)));
+      const uint32_t sb = mx_scale_byte(mb);
+      const float inv = mx_inv_scale(sb);
+      uint32_t c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, mx_scaled(v[0], inv, sb), mx_scaled(v[1], inv, sb), 1.0f, 0) & 0xffu;
+      c |= static_cast<uint32_t>(__shfl_xor(static_cast<int>(c), 1, kWave)) << 8;   // even lanes: two bytes
+      c |= static_cast<uint32_t>(__shfl_xor(static_cast<int>(c), 2, kWave)) << 16;  // lanes 0 mod 4: four
+      if (t < m) {
+        const size_t P = R.base[R.nslots];
+        uint8_t* ac = A.act + static_cast<size_t>(base) * A.I / 2 + (static_cast<size_t>(kb) * m + t) * 16;
+        if (p % 4 == 0) *reinterpret_cast<uint32_t*>(ac + p) = c;
+        if (p == 0) A.act[P * A.I / 2 + static_cast<size_t>(base) * (A.I / 32) + static_cast<size_t>(kb) * m + t] = static_cast<uint8_t>(sb);
+      }
+    } else if (t < m) {
+      const int q = 2 * p;
+      uint8_t* ac = A.act + static_cast<size_t>(base) * A.I * 2 + ((static_cast<size_t>(kb) * 4 + q / 8) * m + t) * 16 + (q % 8) * 2;
+      *reinterpret_cast<uint32_t*>(ac) = pack_bf16x2(v[0], v[1]);
+    }
+  }
+}
+
+// GEMM2 and combine of 16 * nrb output columns for all slots: a wavefront
+// takes (slot, 16 columns) jobs, the pairs' y (rounded to bf16) meet in LDS,
+// and each output is the rank-ordered sum of combine_token.
+template <bool MX, bool OUT_BF16>
+__device__ __forceinline__ void few_gemm2(const FewArgs& A, FewRoute& R, int task, int nrb) {
+  const int lane = lane_id(), r = lane & 15, g = lane >> 4, cols = 16 * nrb;
+  const size_t P = R.base[R.nslots];
+  __syncthreads();  // y free
+  for (int job = wave_id(); job < R.nslots * nrb; job += 4) {
+    const int slot = uniform(job / nrb), rb = uniform(job % nrb), nb = task * nrb + rb;
+    const int e = uniform(R.slot_e[slot]), base = uniform(R.base[slot]), m = uniform(R.base[slot + 1]) - base;
+    const int rr = min(r, m - 1);
+    f32x4 acc;
+    if constexpr (MX) {
+      const int KB = A.I / 128;
+      const uint8_t* w = A.w2 + e * mx_mat_codes(A.d, A.I) + static_cast<size_t>(nb) * KB * 1024 + lane * 16;
+      const uint8_t* ws = A.w2s + e * mx_mat_scales(A.d, A.I) + static_cast<size_t>(nb / 4) * mx_kq(A.I) * 1024 + lane * 4 + nb % 4;
+      const uint8_t* b = A.act + static_cast<size_t>(base) * A.I / 2 + (static_cast<size_t>(g) * m + rr) * 16;
+      const uint8_t* bs = A.act + P * A.I / 2 + static_cast<size_t>(base) * (A.I / 32) + static_cast<size_t>(g) * m + rr;
+      acc = few_stream<true, 8>(w, b, 64 * m, ws, bs, 4 * m, KB);
+    } else {
+      const int KB = A.I / 32;
+      const uint8_t* w = A.w2 + (static_cast<size_t>(e) * A.d * A.I + frag_offset(nb, 0, KB)) * 2 + lane * 16;
+      const uint8_t* b = A.act + static_cast<size_t>(base) * A.I * 2 + (static_cast<size_t>(g) * m + rr) * 16;
+      acc = few_stream<false, 8>(w, b, 64 * m, nullptr, nullptr, 0, KB);
+    }
+    if (r < m)
+      *reinterpret_cast<u32x2*>(R.y + (base + r) * cols + rb * 16 + 4 * g) =
+          u32x2{pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3])};
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < A.T * cols / 2; i += 256) {
+    const int t = i / (cols / 2), c = i % (cols / 2) * 2;
+    float a0 = 0.f, a1 = 0.f;
+    for (int j = 0; j < A.k; ++j) {
+      const int row = R.row[t * A.k + j];
+      if (row < 0) continue;
+      const uint32_t v = *reinterpret_cast<const uint32_t*>(R.y + row * cols + c);
+      const float wj = R.val[t * A.k + j];
+      a0 = fmaf(wj, __uint_as_float(v << 16), a0);
+      a1 = fmaf(wj, __uint_as_float(v & 0xffff0000u), a1);
+    }
+    const size_t at = static_cast<size_t>(t) * A.d + static_cast<size_t>(task) * cols + c;
+    if constexpr (OUT_BF16) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(A.out) + at) = pack_bf16x2(a0, a1);
+    else *reinterpret_cast<f32x2*>(static_cast<float*>(A.out) + at) = f32x2{a0, a1};
+  }
+}
+
+template <bool MX, bool GATED>
+__global__ __launch_bounds__(256, 2) void few_gemm1_kernel(FewArgs A) {
+  __shared__ FewRoute R;
+  __shared__ float h[64 * kHStride];
+  few_route(A, R, 256, blockIdx.x == 0);
+  const int per = (GATED ? 2 : 1) * A.I / 64, n = uniform(R.nslots) * per;
+  for (int i = blockIdx.x; i < n; i += gridDim.x) few_gemm1<MX, GATED>(A, R, h, uniform(i / per), uniform(i % per));
+}
+
+template <bool MX, bool OUT_BF16>
+__global__ __launch_bounds__(256, 2) void few_gemm2_kernel(FewArgs A) {
+  __shared__ FewRoute R;
+  few_route(A, R, 256, false);
+  const int ns = uniform(R.nslots), nrb = ns >= 4 ? 1 : (ns >= 2 ? 2 : 4), n = A.d / (16 * nrb);
+  for (int i = blockIdx.x; i < n; i += gridDim.x) few_gemm2<MX, OUT_BF16>(A, R, i, nrb);
+}
+
+template <bool XBF, bool MX>
+hipError_t front(const FewArgs& A, hipStream_t s) {
+  const int jobs = (A.E + 15) / 16 * A.splits, nlog = XBF ? (jobs + 3) / 4 : (A.E + 15) / 16;
+  const int stage = (A.T * (A.d / 8) + 255) / 256;
+  few_front_kernel<XBF, MX><<<nlog + stage, 256, 0, s>>>(A, nlog);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_forward_few(const moe_problem_t& p, const WsLayout& L, const void* x, const void* packed, bool mx,
+                              const float* bias, int32_t* topk_idx, float* topk_w, float* logits, void* out, char* ws,
+                              hipStream_t s) {
+  if (p.T == 0) return hipSuccess;
+  const bool xbf = p.x_dtype == MOE_BF16, gated = gate_rows(p) == 2, obf = p.out_dtype == MOE_BF16;
+  const uint8_t* base = static_cast<const uint8_t*>(packed);
+  FewArgs A{};
+  A.x = x;
+  A.wg = packed;
+  A.bias = bias;
+  if (mx) {
+    const PackedMxLayout PL = packed_mx_layout(p.d, p.I, p.E_global, p.E_local, xbf, gate_rows(p));
+    A.w13 = base + PL.w13;
+    A.w13s = base + PL.w13s;
+    A.w2 = base + PL.w2;
+    A.w2s = base + PL.w2s;
+  } else {
+    const PackedLayout PL = packed_layout(p.d, p.I, p.E_global, p.E_local, xbf, gate_rows(p));
+    A.w13 = base + PL.w13;
+    A.w2 = base + PL.w2;
+  }
+  A.partial = reinterpret_cast<float*>(ws + L.logits);
+  A.xs = reinterpret_cast<uint8_t*>(ws + L.xbf);
+  A.act = reinterpret_cast<uint8_t*>(ws + L.act);
+  A.topk_idx = topk_idx;
+  A.topk_w = topk_w;
+  A.logits = logits;
+  A.out = out;
+  A.T = p.T;
+  A.d = p.d;
+  A.I = p.I;
+  A.E = p.E_global;
+  A.k = p.k;
+  A.e_begin = p.e_begin;
+  A.E_local = p.E_local;
+  A.splits = router_splits(p.d, p.E_global, xbf);
+  hipError_t e = xbf ? (mx ? front<true, true>(A, s) : front<true, false>(A, s))
+                     : (mx ? front<false, true>(A, s) : front<false, false>(A, s));
+  if (e != hipSuccess) return e;
+  int dev = 0, cus = 0;
+  if ((e = hipGetDevice(&dev)) != hipSuccess) return e;
+  if ((e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev)) != hipSuccess) return e;
+  // most slots a batch can touch
+  const int slots = min(p.E_local, p.T * p.k);
+  const int n1 = slots * (gate_rows(p) * p.I / 64), n2 = p.d / 16;
+  auto g1 = mx ? (gated ? few_gemm1_kernel<true, true> : few_gemm1_kernel<true, false>)
+               : (gated ? few_gemm1_kernel<false, true> : few_gemm1_kernel<false, false>);
+  g1<<<min(n1, 2 * cus), 256, 0, s>>>(A);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  auto g2 = mx ? (obf ? few_gemm2_kernel<true, true> : few_gemm2_kernel<true, false>)
+               : (obf ? few_gemm2_kernel<false, true> : few_gemm2_kernel<false, false>);
+  g2<<<min(n2, 2 * cus), 256, 0, s>>>(A);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -363,6 +363,37 @@ moe_status_t moe_expert_ffn_mxfp4(const moe_problem_t* p, const uint8_t* codes, 
                                      out, static_cast<char*>(ws), static_cast<hipStream_t>(stream)));
 }
 
+namespace {
+
+// moe_forward_few, and with mx moe_forward_few_mxfp4.
+moe_status_t forward_few_call(const moe_problem_t* p, const void* x, const void* packed, bool mx, const float* bias,
+                              int32_t* topk_idx, float* topk_w, float* logits, void* out, void* ws, size_t ws_bytes,
+                              moe_stream_t stream) {
+  moe_status_t st = mx ? check_mx(p) : check_problem(p);
+  if (st != MOE_OK) return st;
+  if (p->T > MOE_FEW_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
+  if (p->T > 0 && (!x || !packed || !topk_idx || !topk_w || !out)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(packed) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
+  WsLayout L;
+  if ((st = check_ws(p, ws, ws_bytes, &L)) != MOE_OK) return st;
+  return hip_status(launch_forward_few(*p, L, x, packed, mx, bias, topk_idx, topk_w, logits, out,
+                                       static_cast<char*>(ws), static_cast<hipStream_t>(stream)));
+}
+
+}  // namespace
+
+moe_status_t moe_forward_few(const moe_problem_t* p, const void* x, const void* packed, const float* bias,
+                             int32_t* topk_idx, float* topk_w, float* logits, void* out, void* ws, size_t ws_bytes,
+                             moe_stream_t stream) {
+  return forward_few_call(p, x, packed, false, bias, topk_idx, topk_w, logits, out, ws, ws_bytes, stream);
+}
+
+moe_status_t moe_forward_few_mxfp4(const moe_problem_t* p, const void* x, const void* packed, const float* bias,
+                                   int32_t* topk_idx, float* topk_w, float* logits, void* out, void* ws,
+                                   size_t ws_bytes, moe_stream_t stream) {
+  return forward_few_call(p, x, packed, true, bias, topk_idx, topk_w, logits, out, ws, ws_bytes, stream);
+}
+
 moe_status_t moe_combine(const moe_problem_t* p, const void* y, const int32_t* pair_pos,
                          const float* topk_w, void* out, moe_stream_t stream) {
   moe_status_t st = check_problem(p);

@@ -218,6 +218,11 @@ hipError_t launch_ffn_mxfp4(const moe_problem_t& p, const WsLayout& L, const uin
                             const int32_t* pair_pos, const float* topk_w, void* y, void* out, char* ws,
                             hipStream_t s);
 
+// The whole layer for T <= MOE_FEW_MAX_TOKENS; mx: packed holds MXFP4 experts.
+hipError_t launch_forward_few(const moe_problem_t& p, const WsLayout& L, const void* x, const void* packed, bool mx,
+                              const float* bias, int32_t* topk_idx, float* topk_w, float* logits, void* out, char* ws,
+                              hipStream_t s);
+
 hipError_t launch_combine(const moe_problem_t& p, const void* y, const int32_t* pair_pos,
                           const float* topk_w, void* out, hipStream_t s);
 

@@ -40,7 +40,7 @@ EXPORTED = (
     "moe_probe_copy", "moe_expert_ffn_waved_save_h", "moe_backward_saved_h", "moe_saved_h_bytes",
     "moe_mxfp4_codes_stride", "moe_mxfp4_scales_stride", "moe_quantize_mxfp4", "moe_dequantize_mxfp4",
     "moe_packed_mxfp4_size", "moe_pack_weights_mxfp4", "moe_unpack_weights_mxfp4",
-    "moe_expert_ffn_mxfp4",
+    "moe_expert_ffn_mxfp4", "moe_forward_few", "moe_forward_few_mxfp4",
     "moe_check_error", "moe_status_string", "moe_version",
 )
 
@@ -115,6 +115,8 @@ def lib() -> ctypes.CDLL:
             "moe_pack_weights_mxfp4": (st, [P, vp, vp, vp, vp, vp, vp]),
             "moe_unpack_weights_mxfp4": (st, [P, vp, vp, vp, vp, vp]),
             "moe_expert_ffn_mxfp4": (st, [P, vp, vp, vp, i32p, i32p, i32p, f32p, vp, vp, vp, ctypes.c_size_t, vp]),
+            "moe_forward_few": (st, [P, vp, vp, f32p, i32p, f32p, f32p, vp, vp, ctypes.c_size_t, vp]),
+            "moe_forward_few_mxfp4": (st, [P, vp, vp, f32p, i32p, f32p, f32p, vp, vp, ctypes.c_size_t, vp]),
             "moe_probe_mfma": (st, [f32p, ctypes.c_size_t, ctypes.c_int32, ctypes.POINTER(ctypes.c_double), vp]),
             "moe_probe_copy": (st, [vp, vp, ctypes.c_size_t, vp]),
             "moe_check_error": (st, [vp, vp]),
@@ -572,3 +574,31 @@ def forward(p: Problem, x, packed, ws, bias=None, serial=False, want_logits=Fals
     y, out = ffn_waved(p, x, packed, disp, w, ws, fused_combine=True, serial=serial, persistent=persistent,
                        save_h=save_h)
     return {"idx": idx, "w": w, "logits": logits, "disp": disp, "y": y, "out": out}
+
+
+FEW_MAX_TOKENS = 16
+
+
+def forward_few(p: Problem, x, packed, ws, bias=None, want_logits=False, mxfp4=False, out=None):
+    """The whole layer for at most FEW_MAX_TOKENS tokens: the results of
+    forward (packed from pack_weights) or, with mxfp4=True, of forward_mxfp4
+    (packed from pack_weights_mxfp4), bit for bit, in fewer and shorter
+    kernels.  Returns idx, w, logits and out."""
+    _need("x", x, (p.T, p.d), _TORCH_DTYPE[p.x_dtype])
+    _need("packed", packed, (packed_mxfp4_size(p) if mxfp4 else packed_weights_size(p),), torch.uint8)
+    _need_workspace(p, ws)
+    if bias is not None:
+        _need("bias", bias, (p.E_global,), torch.float32)
+    dev = x.device
+    idx = torch.empty((p.T, p.k), dtype=torch.int32, device=dev)
+    w = torch.empty((p.T, p.k), dtype=torch.float32, device=dev)
+    logits = torch.empty((p.T, p.E_global), dtype=torch.float32, device=dev) if want_logits else None
+    if out is None:
+        out = torch.empty((p.T, p.d), dtype=_out_dtype(p), device=dev)
+    else:
+        _need("out", out, (p.T, p.d), _out_dtype(p))
+    f, name = ((lib().moe_forward_few_mxfp4, "moe_forward_few_mxfp4") if mxfp4
+               else (lib().moe_forward_few, "moe_forward_few"))
+    _check(f(ctypes.byref(p), _p(x), _p(packed), _p(bias), _p(idx), _p(w), _p(logits), _p(out), _p(ws), ws.numel(),
+             _stream()), name)
+    return {"idx": idx, "w": w, "logits": logits, "out": out}

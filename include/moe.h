@@ -378,6 +378,26 @@ moe_status_t moe_expert_ffn_mxfp4(const moe_problem_t* p, const uint8_t* codes, 
                                   const int32_t* pair_pos, const float* topk_w, void* y, void* out, void* ws,
                                   size_t ws_bytes, moe_stream_t stream);
 
+/* The whole layer for a few tokens (a decode step): x to routing and output,
+ * without dispatch tables.  The results are those of the composed calls bit
+ * for bit: topk_idx, topk_w and logits of moe_route; out of
+ * moe_expert_ffn_waved after moe_dispatch (moe_forward_few, packed from
+ * moe_pack_weights), or of moe_quantize_mxfp4 and moe_expert_ffn_mxfp4
+ * (moe_forward_few_mxfp4, packed from moe_pack_weights_mxfp4).
+ *   0 <= T <= MOE_FEW_MAX_TOKENS (MOE_ERR_UNSUPPORTED beyond).
+ *   x, bias, topk_idx, topk_w, logits (NULL: not written): as moe_route;
+ *   out [T, d] in out_dtype.  ws: the forward workspace; nothing in it needs
+ *   a value before the call, and what moe_dispatch left there for other
+ *   calls is no longer valid after it.  Calls that overlap on one workspace
+ *   race. */
+#define MOE_FEW_MAX_TOKENS 16
+moe_status_t moe_forward_few(const moe_problem_t* p, const void* x, const void* packed, const float* bias,
+                             int32_t* topk_idx, float* topk_w, float* logits, void* out, void* ws, size_t ws_bytes,
+                             moe_stream_t stream);
+moe_status_t moe_forward_few_mxfp4(const moe_problem_t* p, const void* x, const void* packed, const float* bias,
+                                   int32_t* topk_idx, float* topk_w, float* logits, void* out, void* ws,
+                                   size_t ws_bytes, moe_stream_t stream);
+
 /* Combine (digest section 1.1; 10100.com deterministic operators): for each
  * token, out[t] = sum over ranks j = 0..k-1 with pair_pos[t, j] >= 0 of
  * topk_w[t, j] * y[pair_pos[t, j]], accumulated in fp32 with fused
