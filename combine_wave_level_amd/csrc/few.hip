@@ -10,11 +10,12 @@
 // k-group of all rows side by side), so that one matrix instruction's operand
 // is at most 1 KiB of consecutive memory, from the caches.
 //
-// Results are those of the composed path bit for bit (moe_route_dispatch,
-// then moe_expert_ffn_waved or moe_quantize_mxfp4 and moe_expert_ffn_mxfp4):
-// the same matrix instruction over the same unsplit ascending K for every
-// output element, the same partial sums of the router, the same selection
-// order, activation, roundings and combine order.
+// The routing is that of moe_route bit for bit (the same chains of matrix
+// instructions, partial sums and selection order), and the expert products
+// that of the composed path: the same instruction over the same unsplit
+// ascending K for every element.  The one difference is that the pairs' y
+// never leave the chip here, so they are not rounded to bf16 before the
+// combine.
 #include "ffn_parts.h"
 #include "moe_internal.h"
 #include "mxfp4.h"
@@ -45,6 +46,44 @@ struct FewArgs {
   int T, d, I, E, k, e_begin, E_local, splits;
 };
 
+// ------------------------------------------------------------------ the stream
+
+// One wavefront: 16 weight rows times the slot's tokens over the whole K.
+// w: the row block's fragments for this lane (1 KiB apart); b: this lane's
+// piece of the token operand, bstep bytes apart (a row past the slot's rows
+// repeats a valid one: its column is not used); MX: ws, bs the scale bytes,
+// 256 and bsstep bytes apart.  U fragments are in flight.
+template <bool MX, int U>
+__device__ __forceinline__ f32x4 few_stream(const uint8_t* __restrict__ w, const uint8_t* __restrict__ b, size_t bstep,
+                                            const uint8_t* __restrict__ ws, const uint8_t* __restrict__ bs,
+                                            size_t bsstep, int n) {
+  u32x4 ra[U], rb[U];
+  uint32_t sa[U], sb[U];
+  auto load = [&](int u, int i) {
+    i = min(i, n - 1);
+    ra[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w + static_cast<size_t>(i) * 1024));
+    rb[u] = ld16(b + static_cast<size_t>(i) * bstep);
+    if constexpr (MX) {
+      sa[u] = ws[static_cast<size_t>(i) * 256];
+      sb[u] = bs[static_cast<size_t>(i) * bsstep];
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(u, u);
+  f32x4 acc{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < n; i += U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i + u < n) {
+        if constexpr (MX) acc = mfma_mx<0, 0>(ra[u], rb[u], acc, sa[u], sb[u]);
+        else acc = mfma16x16x32(ra[u], rb[u], acc);
+      }
+      load(u, i + u + U);
+    }
+  }
+  return acc;
+}
+
 // ------------------------------------------------------------------ kernel 1
 
 // Partial logits of 16 experts over one range of d by one wavefront: the
@@ -55,9 +94,8 @@ __device__ __forceinline__ void few_logits_bf16(const FewArgs& A, int job) {
   const int ks = A.d / A.splits / 32, kb0 = sp * ks;
   const uint16_t* w = static_cast<const uint16_t*>(A.wg) + frag_offset(eb, kb0, A.d / 32) + lane * 8;
   const uint16_t* xr = static_cast<const uint16_t*>(A.x) + static_cast<size_t>(min(r, A.T - 1)) * A.d + kb0 * 32 + g * 8;
-  f32x4 acc{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-  for (int i = 0; i < ks; ++i) acc = mfma16x16x32(ld16(w + i * 512), ld16(xr + i * 32), acc);
+  const f32x4 acc = few_stream<false, 16>(reinterpret_cast<const uint8_t*>(w), reinterpret_cast<const uint8_t*>(xr), 64,
+                                          nullptr, nullptr, 0, ks);
   if (r < A.T) {
     float* o = A.partial + (static_cast<size_t>(sp) * A.T + r) * A.E;
 #pragma unroll
@@ -163,17 +201,11 @@ __global__ __launch_bounds__(256) void few_front_kernel(FewArgs A, int nlog) {
 
 // ------------------------------------------------------------------ routing in LDS
 
-// What every workgroup of the expert kernels derives from the partial logits
-// for itself (a few microseconds less than another kernel): the picks, their
-// weights, and the touched local experts ("slots") with their rows.
+// What every workgroup of the expert kernels derives for itself: the picks,
+// their weights, and the touched local experts ("slots") with their rows.
 struct FewRoute {
-  union {
-    float logit[kFew * kMaxE];
-    uint16_t y[kFew * kMaxK * 16];  // later: the pairs' outputs for 16 columns
-  };
   int32_t idx[kFew * kMaxK];
-  float val[kFew * kMaxK];     // logit, then weight
-  float ex[kFew * kMaxK];
+  float val[kFew * kMaxK];     // weights
   int16_t row[kFew * kMaxK];   // pair -> pair row, -1: expert not local
   uint32_t mask[kMaxE];        // per local expert: the tokens that pick it
   int16_t slot_of[kMaxE];
@@ -182,58 +214,108 @@ struct FewRoute {
   int nslots;
 };
 
-__device__ __forceinline__ void few_route(const FewArgs& A, FewRoute& R, int nthreads, bool write) {
-  const int tid = threadIdx.x, TE = A.T * A.E, TK = A.T * A.k;
-  for (int i = tid; i < TE; i += nthreads) {
-    float acc = A.partial[i];
-    for (int sp = 1; sp < A.splits; ++sp) acc += A.partial[static_cast<size_t>(sp) * TE + i];
-    if (A.bias) acc += A.bias[i % A.E];
-    R.logit[i] = acc;
-    if (write && A.logits) A.logits[i] = acc;
+// Largest value over the wavefront, by the lane shifts of the vector ALU.
+__device__ __forceinline__ float wave_max(float v) {
+#define MOE_STEP(ctrl) \
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(v), __float_as_int(v), ctrl, 0xf, 0xf, false)))
+  MOE_STEP(0x111);  // row_shr 1, 2, 4, 8
+  MOE_STEP(0x112);
+  MOE_STEP(0x114);
+  MOE_STEP(0x118);
+  MOE_STEP(0x142);  // row_bcast 15, 31
+  MOE_STEP(0x143);
+#undef MOE_STEP
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+// topk_token's selection for token t by one wavefront, with the same picks
+// and the same weights: k rounds of the largest value, ties to the lower
+// expert, NaN never; a token without enough comparable logits is left
+// 0x7fffffff and its weights come out NaN as there.  (k rounds of topk_token's
+// lane exchanges took several times as long, in every workgroup.)
+__device__ __forceinline__ void few_topk(const FewArgs& A, FewRoute& R, int t, bool write) {
+  const int lane = lane_id();
+  float v[4];
+  bool live[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int e = lane + 64 * q;
+    live[q] = e < A.E;
+    v[q] = 0.f;
+    if (live[q]) {
+      float acc = A.partial[static_cast<size_t>(t) * A.E + e];
+      for (int sp = 1; sp < A.splits; ++sp) acc += A.partial[(static_cast<size_t>(sp) * A.T + t) * A.E + e];
+      if (A.bias) acc += A.bias[e];
+      if (write && A.logits) A.logits[static_cast<size_t>(t) * A.E + e] = acc;
+      v[q] = acc;
+    }
+    live[q] = live[q] && v[q] == v[q];
   }
-  // a token without enough comparable logits (NaN) picks no expert there, as
-  // topk_token leaves it
-  for (int i = tid; i < TK; i += nthreads) {
-    R.idx[i] = 0x7fffffff;
-    R.val[i] = -__builtin_inff();
-  }
-  for (int i = tid; i < kMaxE; i += nthreads) R.mask[i] = 0;
-  __syncthreads();
-  // rank of each expert by counting the better ones (NaN is never better)
-  for (int i = tid; i < TE; i += nthreads) {
-    const int t = i / A.E, e = i % A.E;
-    const float v = R.logit[i];
-    const float* row = R.logit + t * A.E;
-    int rank = 0;
-    for (int o = 0; o < A.E; ++o) rank += topk_better(row[o], o, v, e) ? 1 : 0;
-    if (v == v && rank < A.k) {
-      R.idx[t * A.k + rank] = e;
-      R.val[t * A.k + rank] = v;
+  float my_v = -__builtin_inff();
+  int my_i = 0x7fffffff;
+  for (int j = 0; j < A.k; ++j) {
+    float bv = -__builtin_inff();
+    int bq = 4;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (live[q] && (bq == 4 || v[q] > bv)) {
+        bv = v[q];
+        bq = q;
+      }
+    const float best = wave_max(bv);
+    int win = 0x7fffffff;
+#pragma unroll
+    for (int q = 3; q >= 0; --q) {
+      const unsigned long long m = __ballot(bq == q && bv == best);
+      if (m) win = 64 * q + __ffsll(m) - 1;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (lane + 64 * q == win) live[q] = false;
+    if (lane == j) {
+      my_v = best;
+      my_i = win;
     }
   }
-  __syncthreads();
-  for (int i = tid; i < TK; i += nthreads) {
-    const int t = i / A.k, le = R.idx[i] - A.e_begin;
-    R.ex[i] = expf(R.val[i] - R.val[t * A.k]);
-    if (le >= 0 && le < A.E_local) atomicOr(&R.mask[le], 1u << t);
-  }
-  __syncthreads();
-  for (int i = tid; i < TK; i += nthreads) {
-    const float* ex = R.ex + i / A.k * A.k;
-    float sum = 0.f;
-    for (int j = 0; j < A.k; ++j) sum += ex[j];  // ascending rank order
-    const float w = R.ex[i] / sum;
-    R.val[i] = w;
+  const float vmax = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_v), 0));
+  const float ex = lane < A.k ? expf(my_v - vmax) : 0.f;
+  float sum = 0.f;
+  for (int j = 0; j < A.k; ++j) sum += __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ex), j));  // ascending
+  if (lane < A.k) {
+    const float w = ex / sum;
+    R.idx[t * A.k + lane] = my_i;
+    R.val[t * A.k + lane] = w;
     if (write) {
-      A.topk_idx[i] = R.idx[i];
-      A.topk_w[i] = w;
+      A.topk_idx[t * A.k + lane] = my_i;
+      A.topk_w[t * A.k + lane] = w;
     }
   }
+}
+
+// FROM_LOGITS: selects from the partial logits; else takes the picks and
+// weights that the first expert kernel wrote.
+template <int NT, bool FROM_LOGITS>
+__device__ __forceinline__ void few_route(const FewArgs& A, FewRoute& R, bool write) {
+  const int tid = threadIdx.x, TK = A.T * A.k;
+  for (int i = tid; i < kMaxE; i += NT) R.mask[i] = 0;
+  if constexpr (FROM_LOGITS) {
+    for (int t = uniform(wave_id()); t < A.T; t += NT / kWave) few_topk(A, R, t, write);
+  } else {
+    for (int i = tid; i < TK; i += NT) {
+      R.idx[i] = A.topk_idx[i];
+      R.val[i] = A.topk_w[i];
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < TK; i += NT) {
+    const int le = R.idx[i] - A.e_begin;
+    if (le >= 0 && le < A.E_local) atomicOr(&R.mask[le], 1u << (i / A.k));
+  }
+  __syncthreads();
   if (wave_id() == 0) {
     const int lane = lane_id();
     int slots = 0, rows = 0;
-#pragma unroll
-    for (int c = 0; c < kMaxE / kWave; ++c) {
+    for (int c = 0; c * kWave < A.E_local; ++c) {
       const int e = c * kWave + lane, n = __popc(R.mask[e]);
       int incl = n;
 #pragma unroll
@@ -257,7 +339,7 @@ __device__ __forceinline__ void few_route(const FewArgs& A, FewRoute& R, int nth
     }
   }
   __syncthreads();
-  for (int i = tid; i < TK; i += nthreads) {
+  for (int i = tid; i < TK; i += NT) {
     const int t = i / A.k, le = R.idx[i] - A.e_begin;
     R.row[i] = le >= 0 && le < A.E_local
                    ? static_cast<int16_t>(R.base[R.slot_of[le]] + __popc(R.mask[le] & ((1u << t) - 1)))
@@ -270,44 +352,6 @@ __device__ __forceinline__ void few_route(const FewArgs& A, FewRoute& R, int nth
 __device__ __forceinline__ int nth_bit(uint32_t mask, int r) {
   for (int i = 0; i < r; ++i) mask &= mask - 1;
   return __ffs(mask) - 1;
-}
-
-// ------------------------------------------------------------------ the stream
-
-// One wavefront: 16 weight rows times the slot's tokens over the whole K.
-// w: the row block's fragments for this lane (1 KiB apart); b: this lane's
-// piece of the token operand, bstep bytes apart (a row past the slot's rows
-// repeats a valid one: its column is not used); MX: ws, bs the scale bytes,
-// 256 and bsstep bytes apart.  U fragments are in flight.
-template <bool MX, int U>
-__device__ __forceinline__ f32x4 few_stream(const uint8_t* __restrict__ w, const uint8_t* __restrict__ b, size_t bstep,
-                                            const uint8_t* __restrict__ ws, const uint8_t* __restrict__ bs,
-                                            size_t bsstep, int n) {
-  u32x4 ra[U], rb[U];
-  uint32_t sa[U], sb[U];
-  auto load = [&](int u, int i) {
-    i = min(i, n - 1);
-    ra[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w + static_cast<size_t>(i) * 1024));
-    rb[u] = ld16(b + static_cast<size_t>(i) * bstep);
-    if constexpr (MX) {
-      sa[u] = ws[static_cast<size_t>(i) * 256];
-      sb[u] = bs[static_cast<size_t>(i) * bsstep];
-    }
-  };
-#pragma unroll
-  for (int u = 0; u < U; ++u) load(u, u);
-  f32x4 acc{0.f, 0.f, 0.f, 0.f};
-  for (int i = 0; i < n; i += U) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (i + u < n) {
-        if constexpr (MX) acc = mfma_mx<0, 0>(ra[u], rb[u], acc, sa[u], sb[u]);
-        else acc = mfma16x16x32(ra[u], rb[u], acc);
-      }
-      load(u, i + u + U);
-    }
-  }
-  return acc;
 }
 
 constexpr int kHStride = 17;  // floats per row of the h exchange
@@ -349,7 +393,8 @@ __device__ __forceinline__ void few_gemm1(const FewArgs& A, const FewRoute& R, f
       const int q = 2 * p + i;  // element of the block
       if constexpr (GATED) {
         const int hr = (q / 16) * 32 + q % 16;
-        v[i] = silu_mul(h[hr * kHStride + t], h[(hr + 16) * kHStride + t]);
+        const float h1 = h[hr * kHStride + t], h3 = h[(hr + 16) * kHStride + t];
+        v[i] = MX ? mx_silu_mul(h1, h3) : silu_mul(h1, h3);
       } else {
         v[i] = relu_sq(h[(blk * 32 + q) * kHStride + t]);
       }
@@ -378,47 +423,95 @@ __device__ __forceinline__ void few_gemm1(const FewArgs& A, const FewRoute& R, f
   }
 }
 
-// GEMM2 and combine of 16 * nrb output columns for all slots: a wavefront
-// takes (slot, 16 columns) jobs, the pairs' y (rounded to bf16) meet in LDS,
-// and each output is the rank-ordered sum of combine_token.
-template <bool MX, bool OUT_BF16>
-__device__ __forceinline__ void few_gemm2(const FewArgs& A, FewRoute& R, int task, int nrb) {
+// GEMM2 and combine of 16 * nrb output columns for all slots, by NW
+// wavefronts.  A wavefront takes (slot, 16 columns) jobs; its loads run on
+// from one job into the next, so the short reductions of a narrow layer do
+// not drain the stream.  The pairs' y meet in LDS in fp32, and each output
+// is combine_token's rank-ordered sum.
+template <bool MX, bool OUT_BF16, int NW, int U>
+__device__ __forceinline__ void few_gemm2(const FewArgs& A, const FewRoute& R, float* __restrict__ y, int task, int nrb) {
   const int lane = lane_id(), r = lane & 15, g = lane >> 4, cols = 16 * nrb;
   const size_t P = R.base[R.nslots];
-  __syncthreads();  // y free
-  for (int job = wave_id(); job < R.nslots * nrb; job += 4) {
-    const int slot = uniform(job / nrb), rb = uniform(job % nrb), nb = task * nrb + rb;
+  const int KB = MX ? A.I / 128 : A.I / 32, njobs = R.nslots * nrb;
+  const uint8_t *w = nullptr, *b = nullptr, *ws = nullptr, *bs = nullptr;
+  uint32_t bstep = 0, wstep = 0;
+  int ljob = uniform(wave_id()) - NW, left = 0;
+  auto next = [&]() {  // addresses of the next job's first fragment; after the last job, the same one again
+    ljob += NW;
+    if (ljob >= njobs) {
+      if (w) w -= wstep, b -= bstep;
+      if (MX && w) ws -= wstep / 4, bs -= bstep / 16;
+      wstep = bstep = 0;
+      left = 1 << 30;
+      return;
+    }
+    const int slot = uniform(ljob / nrb), nb = task * nrb + uniform(ljob % nrb);
     const int e = uniform(R.slot_e[slot]), base = uniform(R.base[slot]), m = uniform(R.base[slot + 1]) - base;
     const int rr = min(r, m - 1);
-    f32x4 acc;
+    wstep = 1024;
+    bstep = 64 * m;
+    left = KB;
     if constexpr (MX) {
-      const int KB = A.I / 128;
-      const uint8_t* w = A.w2 + e * mx_mat_codes(A.d, A.I) + static_cast<size_t>(nb) * KB * 1024 + lane * 16;
-      const uint8_t* ws = A.w2s + e * mx_mat_scales(A.d, A.I) + static_cast<size_t>(nb / 4) * mx_kq(A.I) * 1024 + lane * 4 + nb % 4;
-      const uint8_t* b = A.act + static_cast<size_t>(base) * A.I / 2 + (static_cast<size_t>(g) * m + rr) * 16;
-      const uint8_t* bs = A.act + P * A.I / 2 + static_cast<size_t>(base) * (A.I / 32) + static_cast<size_t>(g) * m + rr;
-      acc = few_stream<true, 8>(w, b, 64 * m, ws, bs, 4 * m, KB);
+      w = A.w2 + e * mx_mat_codes(A.d, A.I) + static_cast<size_t>(nb) * KB * 1024 + lane * 16;
+      ws = A.w2s + e * mx_mat_scales(A.d, A.I) + static_cast<size_t>(nb / 4) * mx_kq(A.I) * 1024 + lane * 4 + nb % 4;
+      b = A.act + static_cast<size_t>(base) * A.I / 2 + (static_cast<size_t>(g) * m + rr) * 16;
+      bs = A.act + P * A.I / 2 + static_cast<size_t>(base) * (A.I / 32) + static_cast<size_t>(g) * m + rr;
     } else {
-      const int KB = A.I / 32;
-      const uint8_t* w = A.w2 + (static_cast<size_t>(e) * A.d * A.I + frag_offset(nb, 0, KB)) * 2 + lane * 16;
-      const uint8_t* b = A.act + static_cast<size_t>(base) * A.I * 2 + (static_cast<size_t>(g) * m + rr) * 16;
-      acc = few_stream<false, 8>(w, b, 64 * m, nullptr, nullptr, 0, KB);
+      w = A.w2 + (static_cast<size_t>(e) * A.d * A.I + frag_offset(nb, 0, KB)) * 2 + lane * 16;
+      b = A.act + static_cast<size_t>(base) * A.I * 2 + (static_cast<size_t>(g) * m + rr) * 16;
     }
-    if (r < m)
-      *reinterpret_cast<u32x2*>(R.y + (base + r) * cols + rb * 16 + 4 * g) =
-          u32x2{pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3])};
+  };
+  __syncthreads();  // y free
+  if (uniform(wave_id()) < njobs) {
+    u32x4 ra[U], rb[U];
+    uint32_t sa[U], sb[U];
+    auto load = [&](int u) {
+      ra[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w));
+      rb[u] = ld16(b);
+      if constexpr (MX) {
+        sa[u] = *ws;
+        sb[u] = *bs;
+        ws += wstep / 4;
+        bs += bstep / 16;
+      }
+      w += wstep;
+      b += bstep;
+      if (--left == 0) next();
+    };
+    next();
+#pragma unroll
+    for (int u = 0; u < U; ++u) load(u);
+    f32x4 acc{0.f, 0.f, 0.f, 0.f};
+    int job = uniform(wave_id()), todo = KB;
+    while (job < njobs) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (job < njobs) {
+          if constexpr (MX) acc = mfma_mx<0, 0>(ra[u], rb[u], acc, sa[u], sb[u]);
+          else acc = mfma16x16x32(ra[u], rb[u], acc);
+          if (--todo == 0) {
+            const int slot = uniform(job / nrb), base = uniform(R.base[slot]), m = uniform(R.base[slot + 1]) - base;
+            if (r < m) *reinterpret_cast<f32x4*>(y + (base + r) * cols + (job % nrb) * 16 + 4 * g) = acc;
+            acc = f32x4{0.f, 0.f, 0.f, 0.f};
+            job += NW;
+            todo = KB;
+          }
+        }
+        load(u);
+      }
+    }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < A.T * cols / 2; i += 256) {
+  for (int i = threadIdx.x; i < A.T * cols / 2; i += 64 * NW) {
     const int t = i / (cols / 2), c = i % (cols / 2) * 2;
     float a0 = 0.f, a1 = 0.f;
     for (int j = 0; j < A.k; ++j) {
       const int row = R.row[t * A.k + j];
       if (row < 0) continue;
-      const uint32_t v = *reinterpret_cast<const uint32_t*>(R.y + row * cols + c);
+      const f32x2 v = *reinterpret_cast<const f32x2*>(y + row * cols + c);
       const float wj = R.val[t * A.k + j];
-      a0 = fmaf(wj, __uint_as_float(v << 16), a0);
-      a1 = fmaf(wj, __uint_as_float(v & 0xffff0000u), a1);
+      a0 = fmaf(wj, v.x, a0);
+      a1 = fmaf(wj, v.y, a1);
     }
     const size_t at = static_cast<size_t>(t) * A.d + static_cast<size_t>(task) * cols + c;
     if constexpr (OUT_BF16) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(A.out) + at) = pack_bf16x2(a0, a1);
@@ -427,20 +520,29 @@ __device__ __forceinline__ void few_gemm2(const FewArgs& A, FewRoute& R, int tas
 }
 
 template <bool MX, bool GATED>
-__global__ __launch_bounds__(256, 2) void few_gemm1_kernel(FewArgs A) {
+__global__ __launch_bounds__(256, 4) void few_gemm1_kernel(FewArgs A) {
   __shared__ FewRoute R;
   __shared__ float h[64 * kHStride];
-  few_route(A, R, 256, blockIdx.x == 0);
+  few_route<256, true>(A, R, blockIdx.x == 0);
   const int per = (GATED ? 2 : 1) * A.I / 64, n = uniform(R.nslots) * per;
   for (int i = blockIdx.x; i < n; i += gridDim.x) few_gemm1<MX, GATED>(A, R, h, uniform(i / per), uniform(i % per));
 }
 
+constexpr int kFewWaves2 = 8;
+
+// y in LDS: 16 * nrb columns a pair.  nrb is 1 from 8 slots up; with fewer
+// there are at most 16 pairs a slot: 7 * 16 pairs of 32 columns, 3 * 16 of 64
+// or 16 of 128.
+constexpr size_t few_y_bytes(int pairs) { return static_cast<size_t>(pairs * 16 > 3584 ? pairs * 16 : 3584) * 4; }
+
 template <bool MX, bool OUT_BF16>
-__global__ __launch_bounds__(256, 2) void few_gemm2_kernel(FewArgs A) {
+__global__ __launch_bounds__(64 * kFewWaves2, 4) void few_gemm2_kernel(FewArgs A) {
+  extern __shared__ __align__(16) float few_y[];
   __shared__ FewRoute R;
-  few_route(A, R, 256, false);
-  const int ns = uniform(R.nslots), nrb = ns >= 4 ? 1 : (ns >= 2 ? 2 : 4), n = A.d / (16 * nrb);
-  for (int i = blockIdx.x; i < n; i += gridDim.x) few_gemm2<MX, OUT_BF16>(A, R, i, nrb);
+  few_route<64 * kFewWaves2, false>(A, R, false);
+  // enough jobs for the wavefronts: 1, 2, 4 or 8 column blocks
+  const int ns = uniform(R.nslots), nrb = ns >= 8 ? 1 : (ns >= 4 ? 2 : (ns >= 2 ? 4 : 8)), n = A.d / (16 * nrb);
+  for (int i = blockIdx.x; i < n; i += gridDim.x) few_gemm2<MX, OUT_BF16, kFewWaves2, 8>(A, R, few_y, i, nrb);
 }
 
 template <bool XBF, bool MX>
@@ -500,11 +602,11 @@ hipError_t launch_forward_few(const moe_problem_t& p, const WsLayout& L, const v
   const int n1 = slots * (gate_rows(p) * p.I / 64), n2 = p.d / 16;
   auto g1 = mx ? (gated ? few_gemm1_kernel<true, true> : few_gemm1_kernel<true, false>)
                : (gated ? few_gemm1_kernel<false, true> : few_gemm1_kernel<false, false>);
-  g1<<<min(n1, 2 * cus), 256, 0, s>>>(A);
+  g1<<<min(n1, 4 * cus), 256, 0, s>>>(A);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   auto g2 = mx ? (obf ? few_gemm2_kernel<true, true> : few_gemm2_kernel<true, false>)
                : (obf ? few_gemm2_kernel<false, true> : few_gemm2_kernel<false, false>);
-  g2<<<min(n2, 2 * cus), 256, 0, s>>>(A);
+  g2<<<min(n2, 2 * cus), 64 * kFewWaves2, few_y_bytes(p.T * min(p.k, p.E_local)), s>>>(A);
   return hipGetLastError();
 }
 

@@ -38,8 +38,8 @@ __device__ __forceinline__ void mx_store_act(const MxAcc<C>& acc, uint8_t* lds, 
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         if constexpr (GATED) {
-          v[r] = silu_mul(acc.v[q * 4][b][r], acc.v[q * 4 + 1][b][r]);
-          v[4 + r] = silu_mul(acc.v[q * 4 + 2][b][r], acc.v[q * 4 + 3][b][r]);
+          v[r] = mx_silu_mul(acc.v[q * 4][b][r], acc.v[q * 4 + 1][b][r]);
+          v[4 + r] = mx_silu_mul(acc.v[q * 4 + 2][b][r], acc.v[q * 4 + 3][b][r]);
         } else {
           v[r] = relu_sq(acc.v[q * 2][b][r]);
           v[4 + r] = relu_sq(acc.v[q * 2 + 1][b][r]);
@@ -90,12 +90,41 @@ struct MxArgs {
   int E_local, d, I;
 };
 
+// build_mtile_prefix by the first wavefront: its one-thread loop waits out
+// E_local loads in turn, several microseconds before the first tile.
+__device__ __forceinline__ void mx_mtile_prefix(const int32_t* __restrict__ offsets, int E_local, int BT,
+                                                int32_t* mt_pre) {
+  if (wave_id() != 0) return;
+  const int lane = lane_id();
+  int32_t n[kMaxLocalExperts / kWave];
+#pragma unroll
+  for (int c = 0; c < kMaxLocalExperts / kWave; ++c) {
+    const int e = c * kWave + lane;
+    n[c] = e < E_local ? (offsets[e + 1] - offsets[e] + BT - 1) / BT : 0;
+  }
+  int run = 0;
+#pragma unroll
+  for (int c = 0; c < kMaxLocalExperts / kWave; ++c) {
+    if (c * kWave >= E_local) break;
+    int incl = n[c];
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) {
+      const int o = __shfl_up(incl, off, kWave);
+      incl += lane >= off ? o : 0;
+    }
+    if (c * kWave + lane < E_local) mt_pre[c * kWave + lane] = run + incl - n[c];
+    run += __shfl(incl, kWave - 1, kWave);
+  }
+  if (lane == 0) mt_pre[E_local] = run;
+}
+
 // Tile loop of a phase: f(expert, first row, rows, n-tile).
 template <class C, class F>
 __device__ __forceinline__ void mx_tiles(const MxArgs& A, int NT, F f) {
   __shared__ int32_t mt_pre[kMaxLocalExperts + 1];
   __shared__ int32_t xcd_order;
-  build_mtile_prefix(A.offsets, A.E_local, C::BT, mt_pre);
+  mx_mtile_prefix(A.offsets, A.E_local, C::BT, mt_pre);
+  __syncthreads();
   if (threadIdx.x == 0) xcd_order = !C::STREAM && phase_xcd_order(mt_pre, A.E_local);
   __syncthreads();
   const bool xo = uniform(xcd_order) != 0;
