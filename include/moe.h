@@ -370,8 +370,9 @@ moe_status_t moe_unpack_weights_mxfp4(const moe_problem_t* p, const void* packed
  * split; y is rounded to bf16 and combined as moe_combine does.
  *   codes, scales: from moe_quantize_mxfp4 (or the caller), row strides as
  *   there.  packed: from moe_pack_weights_mxfp4.  The rest as
- *   moe_expert_ffn_waved (same workspace after moe_dispatch).  The call runs
- *   the phase schedule and may be repeated on one dispatch; calls that
+ *   moe_expert_ffn_waved (same workspace after moe_dispatch); y also serves as
+ *   scratch, so its rows past the routed ones are undefined after the call.
+ *   The call runs the phase schedule and may be repeated on one dispatch; calls that
  *   overlap on one workspace race. */
 moe_status_t moe_expert_ffn_mxfp4(const moe_problem_t* p, const uint8_t* codes, const uint8_t* scales,
                                   const void* packed, const int32_t* expert_offsets, const int32_t* sorted_token,

@@ -13,6 +13,7 @@ from combine_wave_level_amd import moe
 
 pytestmark = pytest.mark.gpu
 
+GATED, UNGATED = moe.MOE_ACT_SWIGLU, moe.MOE_ACT_RELU2
 DT = {"bf16": (moe.MOE_BF16, torch.bfloat16), "f32": (moe.MOE_F32, torch.float32)}
 
 
@@ -281,3 +282,23 @@ def test_ffn_against_float64(T, d, I, E, k, E_local, x, act):
     _check_out(L, idx, w, out, toks)
     # the standalone combine of the same y
     assert torch.equal(moe.combine(L["p"], y, disp.pair_pos, w_d), out)
+
+
+@pytest.mark.parametrize("d,I,act", [(512, 256, GATED), (640, 384, UNGATED), (256, 128, GATED)])
+def test_a_token_is_the_same_in_any_batch(d, I, act):
+    """T = 1, 40 (64-row tiles) and 700 (256-row tiles): the rows and outputs
+    of the same tokens have the same bits."""
+    print(f"[case] mxfp4 invariance d={d} I={I} act={act}", flush=True)
+    L = _layer(700, d, I, 4, 2, act=act, seed=5)
+    idx, w = _random_routing(L)
+    outs = {}
+    for T, toks in ((700, np.arange(700)), (40, np.arange(330, 370)), (1, np.array([350]))):
+        p = L["p"].replace(T=T)
+        ws = moe.workspace(p)
+        x = L["x"][torch.as_tensor(toks).cuda()].contiguous()
+        disp = moe.dispatch(p, torch.as_tensor(idx[toks]).cuda(), ws)
+        codes, scales = moe.quantize_mxfp4(p, x)
+        outs[T] = moe.ffn_mxfp4(p, codes, scales, L["packed"], disp, torch.as_tensor(w[toks]).cuda(), ws)[1]
+    torch.cuda.synchronize()
+    assert torch.equal(outs[40], outs[700][330:370])
+    assert torch.equal(outs[1], outs[700][350:351])
