@@ -215,9 +215,8 @@ struct FewRoute {
 };
 
 // Largest value over the wavefront, by the lane shifts of the vector ALU.
-__device__ __forceinline__ float wave_max(float v) {
-#define MOE_STEP(ctrl) \
-  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(v), __float_as_int(v), ctrl, 0xf, 0xf, false)))
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#define MOE_STEP(ctrl) v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), ctrl, 0xf, 0xf, true)))
   MOE_STEP(0x111);  // row_shr 1, 2, 4, 8
   MOE_STEP(0x112);
   MOE_STEP(0x114);
@@ -225,55 +224,85 @@ __device__ __forceinline__ float wave_max(float v) {
   MOE_STEP(0x142);  // row_bcast 15, 31
   MOE_STEP(0x143);
 #undef MOE_STEP
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
+}
+
+// Order-preserving integer of a logit; 0 for NaN (never picked), -0 as +0
+// (they tie).
+__device__ __forceinline__ uint32_t logit_key(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return v == v ? b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u) : 0u;
+}
+__device__ __forceinline__ float key_logit(uint32_t k) {
+  return __uint_as_float((k >> 31) ? k ^ 0x80000000u : ~k);
+}
+
+// All tokens' logits into LDS: the partial sums of every element are in
+// flight together (a loop over them waited out a memory round trip for each
+// of up to eight, most of this kernel's time on a small layer), then added in
+// ascending order, then the bias.
+template <int NT>
+__device__ __forceinline__ void few_logits(const FewArgs& A, float* __restrict__ lg, bool write) {
+  const int TE = A.T * A.E;
+  for (int i0 = threadIdx.x; i0 < TE; i0 += 4 * NT) {
+    float p[4][8], bias[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = min(i0 + u * NT, TE - 1);
+#pragma unroll
+      for (int sp = 0; sp < 8; ++sp) p[u][sp] = sp < A.splits ? A.partial[static_cast<size_t>(sp) * TE + i] : 0.f;
+      bias[u] = A.bias ? A.bias[i % A.E] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * NT;
+      if (i >= TE) break;
+      float acc = p[u][0];
+#pragma unroll
+      for (int sp = 1; sp < 8; ++sp)
+        if (sp < A.splits) acc += p[u][sp];
+      if (A.bias) acc += bias[u];
+      lg[i] = acc;
+      if (write && A.logits) A.logits[i] = acc;
+    }
+  }
 }
 
 // topk_token's selection for token t by one wavefront, with the same picks
 // and the same weights: k rounds of the largest value, ties to the lower
 // expert, NaN never; a token without enough comparable logits is left
-// 0x7fffffff and its weights come out NaN as there.  (k rounds of topk_token's
-// lane exchanges took several times as long, in every workgroup.)
-__device__ __forceinline__ void few_topk(const FewArgs& A, FewRoute& R, int t, bool write) {
-  const int lane = lane_id();
-  float v[4];
-  bool live[4];
+// 0x7fffffff and its weights come out NaN as there.  Every workgroup waits for
+// this chain, so a round is kept short: integer keys and lane shifts take
+// 0.1 us, topk_token's lane exchanges of (value, index) pairs several times
+// that.
+__device__ __forceinline__ void few_topk(const FewArgs& A, FewRoute& R, const float* __restrict__ lg, int t, bool write) {
+  const int lane = lane_id(), nq = (A.E + kWave - 1) / kWave;
+  uint32_t key[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int e = lane + 64 * q;
-    live[q] = e < A.E;
-    v[q] = 0.f;
-    if (live[q]) {
-      float acc = A.partial[static_cast<size_t>(t) * A.E + e];
-      for (int sp = 1; sp < A.splits; ++sp) acc += A.partial[(static_cast<size_t>(sp) * A.T + t) * A.E + e];
-      if (A.bias) acc += A.bias[e];
-      if (write && A.logits) A.logits[static_cast<size_t>(t) * A.E + e] = acc;
-      v[q] = acc;
-    }
-    live[q] = live[q] && v[q] == v[q];
+    key[q] = e < A.E ? logit_key(lg[t * A.E + e]) : 0u;
   }
   float my_v = -__builtin_inff();
   int my_i = 0x7fffffff;
   for (int j = 0; j < A.k; ++j) {
-    float bv = -__builtin_inff();
-    int bq = 4;
+    uint32_t mine = key[0];
+    if (nq > 1) mine = max(mine, key[1]);
+    if (nq > 2) mine = max(mine, max(key[2], key[3]));
+    const uint32_t best = wave_max(mine);
+    if (best == 0) break;  // no comparable logit left
+    int win = 0;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (live[q] && (bq == 4 || v[q] > bv)) {
-        bv = v[q];
-        bq = q;
+    for (int q = 3; q >= 0; --q)
+      if (q < nq) {
+        const unsigned long long m = __ballot(key[q] == best);
+        if (m) win = 64 * q + __ffsll(m) - 1;
       }
-    const float best = wave_max(bv);
-    int win = 0x7fffffff;
-#pragma unroll
-    for (int q = 3; q >= 0; --q) {
-      const unsigned long long m = __ballot(bq == q && bv == best);
-      if (m) win = 64 * q + __ffsll(m) - 1;
-    }
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      if (lane + 64 * q == win) live[q] = false;
+      if (q < nq && lane + 64 * q == win) key[q] = 0;
     if (lane == j) {
-      my_v = best;
+      my_v = key_logit(best);
       my_i = win;
     }
   }
@@ -295,11 +324,13 @@ __device__ __forceinline__ void few_topk(const FewArgs& A, FewRoute& R, int t, b
 // FROM_LOGITS: selects from the partial logits; else takes the picks and
 // weights that the first expert kernel wrote.
 template <int NT, bool FROM_LOGITS>
-__device__ __forceinline__ void few_route(const FewArgs& A, FewRoute& R, bool write) {
+__device__ __forceinline__ void few_route(const FewArgs& A, FewRoute& R, float* __restrict__ lg, bool write) {
   const int tid = threadIdx.x, TK = A.T * A.k;
   for (int i = tid; i < kMaxE; i += NT) R.mask[i] = 0;
   if constexpr (FROM_LOGITS) {
-    for (int t = uniform(wave_id()); t < A.T; t += NT / kWave) few_topk(A, R, t, write);
+    few_logits<NT>(A, lg, write);
+    __syncthreads();
+    for (int t = uniform(wave_id()); t < A.T; t += NT / kWave) few_topk(A, R, lg, t, write);
   } else {
     for (int i = tid; i < TK; i += NT) {
       R.idx[i] = A.topk_idx[i];
@@ -339,6 +370,7 @@ __device__ __forceinline__ void few_route(const FewArgs& A, FewRoute& R, bool wr
     }
   }
   __syncthreads();
+  if constexpr (FROM_LOGITS) return;  // the pairs' rows are the combine's
   for (int i = tid; i < TK; i += NT) {
     const int t = i / A.k, le = R.idx[i] - A.e_begin;
     R.row[i] = le >= 0 && le < A.E_local
@@ -521,11 +553,11 @@ __device__ __forceinline__ void few_gemm2(const FewArgs& A, const FewRoute& R, f
 
 template <bool MX, bool GATED>
 __global__ __launch_bounds__(256, 4) void few_gemm1_kernel(FewArgs A) {
+  extern __shared__ __align__(16) float few_h[];  // the logits, then h
   __shared__ FewRoute R;
-  __shared__ float h[64 * kHStride];
-  few_route<256, true>(A, R, blockIdx.x == 0);
+  few_route<256, true>(A, R, few_h, blockIdx.x == 0);
   const int per = (GATED ? 2 : 1) * A.I / 64, n = uniform(R.nslots) * per;
-  for (int i = blockIdx.x; i < n; i += gridDim.x) few_gemm1<MX, GATED>(A, R, h, uniform(i / per), uniform(i % per));
+  for (int i = blockIdx.x; i < n; i += gridDim.x) few_gemm1<MX, GATED>(A, R, few_h, uniform(i / per), uniform(i % per));
 }
 
 constexpr int kFewWaves2 = 8;
@@ -539,10 +571,18 @@ template <bool MX, bool OUT_BF16>
 __global__ __launch_bounds__(64 * kFewWaves2, 4) void few_gemm2_kernel(FewArgs A) {
   extern __shared__ __align__(16) float few_y[];
   __shared__ FewRoute R;
-  few_route<64 * kFewWaves2, false>(A, R, false);
+  few_route<64 * kFewWaves2, false>(A, R, nullptr, false);
   // enough jobs for the wavefronts: 1, 2, 4 or 8 column blocks
   const int ns = uniform(R.nslots), nrb = ns >= 8 ? 1 : (ns >= 4 ? 2 : (ns >= 2 ? 4 : 8)), n = A.d / (16 * nrb);
-  for (int i = blockIdx.x; i < n; i += gridDim.x) few_gemm2<MX, OUT_BF16, kFewWaves2, 8>(A, R, few_y, i, nrb);
+  // Workgroups go to the XCDs in turn.  The four row blocks of an MXFP4 scale
+  // word are given to one XCD, one after the other, so that it is fetched
+  // once; in plain order four XCDs fetched it, a fifth of the bytes more.
+  const int quads = nrb == 1 ? n / 32 * 32 : 0;
+  for (int i = blockIdx.x; i < n; i += gridDim.x) {
+    const int j = i / 8;
+    const int task = i < quads ? (j / 4 * 8 + i % 8) * 4 + j % 4 : i;
+    few_gemm2<MX, OUT_BF16, kFewWaves2, 8>(A, R, few_y, task, nrb);
+  }
 }
 
 template <bool XBF, bool MX>
@@ -602,7 +642,7 @@ hipError_t launch_forward_few(const moe_problem_t& p, const WsLayout& L, const v
   const int n1 = slots * (gate_rows(p) * p.I / 64), n2 = p.d / 16;
   auto g1 = mx ? (gated ? few_gemm1_kernel<true, true> : few_gemm1_kernel<true, false>)
                : (gated ? few_gemm1_kernel<false, true> : few_gemm1_kernel<false, false>);
-  g1<<<min(n1, 4 * cus), 256, 0, s>>>(A);
+  g1<<<min(n1, 4 * cus), 256, max(64 * kHStride, p.T * p.E_global) * sizeof(float), s>>>(A);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   auto g2 = mx ? (obf ? few_gemm2_kernel<true, true> : few_gemm2_kernel<true, false>)
                : (obf ? few_gemm2_kernel<false, true> : few_gemm2_kernel<false, false>);

@@ -230,7 +230,7 @@ __global__ __launch_bounds__(256) void mx_gather_kernel(const uint8_t* __restric
 }
 
 template <class C, bool GATED>
-__global__ __launch_bounds__(C::NTHREADS, C::STREAM ? 2 : 4) void gemm1_mx_kernel(MxArgs A) {
+__global__ __launch_bounds__(C::NTHREADS, C::STREAM ? 3 : 4) void gemm1_mx_kernel(MxArgs A) {
   extern __shared__ __align__(16) uint8_t mx_lds[];
   const int N = (GATED ? 2 : 1) * A.I;
   mx_tiles<C>(A, N / C::BW, [&](int e, int row0, int count, int nt, int prow0) {
@@ -249,7 +249,7 @@ __global__ __launch_bounds__(C::NTHREADS, C::STREAM ? 2 : 4) void gemm1_mx_kerne
 }
 
 template <class C>
-__global__ __launch_bounds__(C::NTHREADS, C::STREAM ? 2 : 4) void gemm2_mx_kernel(MxArgs A) {
+__global__ __launch_bounds__(C::NTHREADS, C::STREAM ? 3 : 4) void gemm2_mx_kernel(MxArgs A) {
   extern __shared__ __align__(16) uint8_t mx_lds[];
   static_assert(static_cast<size_t>(C::BT) * C::BW * 2 <= C::LDS_BYTES, "output stage fits the tile's LDS");
   mx_tiles<C>(A, A.d / C::BW, [&](int e, int row0, int count, int nt, int prow0) {

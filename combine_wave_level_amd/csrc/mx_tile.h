@@ -26,9 +26,12 @@
 //   multiply while it started or ended a tile, and 2.25 such tiles a CU (16
 //   experts of about 1024 rows, 2048 weight rows) take the time of three.
 // MxStream (a few rows an expert, bound by the weights' bytes): 128 x 64, 4
-//   wavefronts of 64 x 32, token rows gathered by the tile, all operands in 5
-//   stages of one K step; two workgroups a CU, so that one loads while the
-//   other starts or ends a tile.
+//   wavefronts of 64 x 32, token rows gathered by the tile, all operands in 4
+//   stages of one K step; three workgroups a CU, so that some load while
+//   another starts or ends a tile (128 tokens on 32 experts of d = 7168, I =
+//   2048: two workgroups with 5 stages took 115 and 56 us for the two
+//   products, three with 4 stages 111 and 51; tiles of 128 rows, which read
+//   the weights of an expert of more than 64 rows once, 112 and 83).
 #pragma once
 
 #include "gemm_tile.h"
@@ -65,13 +68,14 @@ struct MxStream {
   static constexpr bool STREAM = true;
   static constexpr int BW = 128, BT = 64, WR = 2, WT = 2, NW = 4, NTHREADS = 256;
   static constexpr int AW = BW / WR / 16, AT = BT / WT / 16;
-  static constexpr int NST = 5, LW = BW / 16 / NW, LT = BT / 16 / NW;
+  static constexpr int NST = 4, LW = BW / 16 / NW, LT = BT / 16 / NW;
   static constexpr int NQ = BW / 64;
   static constexpr int LS = 1;
   static constexpr int T0 = BW * 64, S0 = T0 + BT * 64, STAGE = S0 + NQ * 256 + BT * 4;
   static constexpr size_t LDS_BYTES = static_cast<size_t>(NST) * STAGE;
   static_assert(NQ == 2 && BT == 64 && NW == 4, "one scale load a wavefront and step");
   static_assert((NST - 2) * (LW + LT + LS) <= 63, "vmcnt");
+  static_assert(3 * (LDS_BYTES + 1280) <= 160 * 1024, "three workgroups a CU, with their tables");
 };
 
 // wave-uniform, kept in scalar registers
