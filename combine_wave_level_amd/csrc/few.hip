@@ -388,33 +388,23 @@ __device__ __forceinline__ int nth_bit(uint32_t mask, int r) {
 
 constexpr int kHStride = 17;  // floats per row of the h exchange
 
-// GEMM1 task: 64 packed rows (32 intermediate indices gated, 64 ungated) of
-// one slot, 16 rows a wavefront; gate and up meet in LDS, and 16 consecutive
-// lanes hold one token's block of 32 for the activation's scale.
+// LDS-only barrier: the loads in flight stay in flight.
+__device__ __forceinline__ void few_lds_barrier() {
+  wait_lgkm0();
+  raw_barrier();
+}
+
+// Activation of a GEMM1 task (64 packed rows: 32 intermediate indices gated,
+// 64 ungated) from the four wavefronts' accumulators: gate and up meet in
+// LDS, and 16 consecutive lanes hold one token's block of 32 for the scale.
 template <bool MX, bool GATED>
-__device__ __forceinline__ void few_gemm1(const FewArgs& A, const FewRoute& R, float* h, int slot, int nq) {
+__device__ __forceinline__ void few_act(const FewArgs& A, const FewRoute& R, float* h, int slot, int nq, const f32x4& acc) {
   const int lane = lane_id(), r = lane & 15, g = lane >> 4;
-  const int e = R.slot_e[slot], base = R.base[slot], m = R.base[slot + 1] - base;
-  const uint32_t mask = R.mask[e];
-  const int N = (GATED ? 2 : 1) * A.I, tok = nth_bit(mask, min(r, m - 1));
-  const int nb = nq * 4 + wave_id();
-  f32x4 acc;
-  if constexpr (MX) {
-    const int KB = A.d / 128;
-    const uint8_t* w = A.w13 + e * mx_mat_codes(N, A.d) + static_cast<size_t>(nb) * KB * 1024 + lane * 16;
-    const uint8_t* ws = A.w13s + e * mx_mat_scales(N, A.d) + static_cast<size_t>(nq) * mx_kq(A.d) * 1024 + lane * 4 + wave_id();
-    const uint8_t* b = A.xs + (static_cast<size_t>(g) * A.T + tok) * 16;
-    const uint8_t* bs = A.xs + static_cast<size_t>(A.T) * A.d / 2 + static_cast<size_t>(g) * A.T + tok;
-    acc = few_stream<true, 8>(w, b, 64 * A.T, ws, bs, 4 * A.T, KB);
-  } else {
-    const int KB = A.d / 32;
-    const uint8_t* w = A.w13 + (static_cast<size_t>(e) * N * A.d + frag_offset(nb, 0, KB)) * 2 + lane * 16;
-    acc = few_stream<false, 8>(w, A.xs + (static_cast<size_t>(g) * A.T + tok) * 16, 64 * A.T, nullptr, nullptr, 0, KB);
-  }
-  __syncthreads();  // h free
+  const int base = R.base[slot], m = R.base[slot + 1] - base;
+  few_lds_barrier();  // h free
 #pragma unroll
   for (int i = 0; i < 4; ++i) h[(wave_id() * 16 + 4 * g + i) * kHStride + r] = acc[i];
-  __syncthreads();
+  few_lds_barrier();
   const int t = threadIdx.x / 16, p = threadIdx.x % 16;  // row of the slot, element pair of a block
   constexpr int NBLK = GATED ? 1 : 2;
 #pragma unroll
@@ -451,6 +441,78 @@ __device__ __forceinline__ void few_gemm1(const FewArgs& A, const FewRoute& R, f
       const int q = 2 * p;
       uint8_t* ac = A.act + static_cast<size_t>(base) * A.I * 2 + ((static_cast<size_t>(kb) * 4 + q / 8) * m + t) * 16 + (q % 8) * 2;
       *reinterpret_cast<uint32_t*>(ac) = pack_bf16x2(v[0], v[1]);
+    }
+  }
+}
+
+// The GEMM1 tasks blockIdx.x, + gridDim.x, ... of n (slot i / per, 64 packed
+// rows i % per), 16 rows a wavefront; the loads run on from one task into the
+// next, as in few_gemm2.
+template <bool MX, bool GATED, int U>
+__device__ __forceinline__ void few_gemm1(const FewArgs& A, const FewRoute& R, float* h, int n, int per) {
+  const int lane = lane_id(), r = lane & 15, g = lane >> 4, wave = uniform(wave_id());
+  const int N = (GATED ? 2 : 1) * A.I, KB = MX ? A.d / 128 : A.d / 32, step = static_cast<int>(gridDim.x);
+  const uint8_t *w = nullptr, *b = nullptr, *ws = nullptr, *bs = nullptr;
+  const uint32_t bstep = 64 * A.T;
+  uint32_t on = 1;  // 0 behind the last task: the same address again
+  int li = static_cast<int>(blockIdx.x) - step, left = 0;
+  if (li + step >= n) return;
+  auto next = [&]() {
+    li += step;
+    if (li >= n) {
+      on = 0;
+      w -= 1024, b -= bstep;
+      if (MX) ws -= 256, bs -= bstep / 16;
+      left = 1 << 30;
+      return;
+    }
+    const int slot = uniform(li / per), nq = uniform(li % per), nb = nq * 4 + wave;
+    const int e = uniform(R.slot_e[slot]), m = uniform(R.base[slot + 1] - R.base[slot]);
+    const int tok = nth_bit(R.mask[e], min(r, m - 1));
+    left = KB;
+    b = A.xs + (static_cast<size_t>(g) * A.T + tok) * 16;
+    if constexpr (MX) {
+      w = A.w13 + e * mx_mat_codes(N, A.d) + static_cast<size_t>(nb) * KB * 1024 + lane * 16;
+      ws = A.w13s + e * mx_mat_scales(N, A.d) + static_cast<size_t>(nq) * mx_kq(A.d) * 1024 + lane * 4 + wave;
+      bs = A.xs + static_cast<size_t>(A.T) * A.d / 2 + static_cast<size_t>(g) * A.T + tok;
+    } else {
+      w = A.w13 + (static_cast<size_t>(e) * N * A.d + frag_offset(nb, 0, KB)) * 2 + lane * 16;
+    }
+  };
+  u32x4 ra[U], rb[U];
+  uint32_t sa[U], sb[U];
+  auto load = [&](int u) {
+    ra[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w));
+    rb[u] = ld16(b);
+    if constexpr (MX) {
+      sa[u] = *ws;
+      sb[u] = *bs;
+      ws += on * 256;
+      bs += on * (bstep / 16);
+    }
+    w += on * 1024;
+    b += on * bstep;
+    if (--left == 0) next();
+  };
+  next();
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(u);
+  f32x4 acc{0.f, 0.f, 0.f, 0.f};
+  int ci = static_cast<int>(blockIdx.x), todo = KB;
+  while (ci < n) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (ci < n) {
+        if constexpr (MX) acc = mfma_mx<0, 0>(ra[u], rb[u], acc, sa[u], sb[u]);
+        else acc = mfma16x16x32(ra[u], rb[u], acc);
+        if (--todo == 0) {
+          few_act<MX, GATED>(A, R, h, uniform(ci / per), uniform(ci % per), acc);
+          acc = f32x4{0.f, 0.f, 0.f, 0.f};
+          ci += step;
+          todo = KB;
+        }
+      }
+      load(u);
     }
   }
 }
@@ -555,9 +617,9 @@ template <bool MX, bool GATED>
 __global__ __launch_bounds__(256, 4) void few_gemm1_kernel(FewArgs A) {
   extern __shared__ __align__(16) float few_h[];  // the logits, then h
   __shared__ FewRoute R;
-  few_route<256, true>(A, R, few_h, blockIdx.x == 0);
+  few_route<256, true>(A, R, few_h, blockIdx.x == 0);  // ends with a barrier: the logits are free
   const int per = (GATED ? 2 : 1) * A.I / 64, n = uniform(R.nslots) * per;
-  for (int i = blockIdx.x; i < n; i += gridDim.x) few_gemm1<MX, GATED>(A, R, few_h, uniform(i / per), uniform(i % per));
+  few_gemm1<MX, GATED, 8>(A, R, few_h, n, per);
 }
 
 constexpr int kFewWaves2 = 8;

@@ -343,10 +343,10 @@ _TORCH_DTYPE = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}
 def _need(name, t, shape, dtype):
     """The library reads dense row-major memory of one type on the current
     GPU: anything else is refused here, where the tensor still says what it is."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape:
         got = f"{t.dtype} {tuple(t.shape)}" if isinstance(t, torch.Tensor) else type(t).__name__
         raise ValueError(f"{name}: {dtype} of shape {tuple(shape)} expected, got {got}")
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name}: on {t.device}, not on the current GPU")
     if not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous (strides {t.stride()})")
