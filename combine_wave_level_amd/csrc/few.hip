@@ -84,6 +84,35 @@ __device__ __forceinline__ f32x4 few_stream(const uint8_t* __restrict__ w, const
   return acc;
 }
 
+// U K steps of operands in flight for RB row blocks.
+template <bool MX, int RB, int U>
+struct FewRing {
+  u32x4 a[U][RB], b[U];
+  uint32_t sa[U], sb[U];
+  // w, w + w1: the row blocks' fragments; ws: their scale words, bs: scale byte
+  __device__ __forceinline__ void load(int u, const uint8_t* w, size_t w1, const uint8_t* t, const uint8_t* ws,
+                                       const uint8_t* bs) {
+    a[u][0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w));
+    if constexpr (RB == 2) a[u][1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w + w1));
+    b[u] = ld16(t);
+    if constexpr (MX) {
+      sa[u] = *reinterpret_cast<const uint32_t*>(ws);
+      sb[u] = *bs;
+    }
+  }
+  // shift: to the first row block's byte of the scale word
+  __device__ __forceinline__ void multiply(int u, f32x4 (&acc)[RB], int shift) const {
+    if constexpr (MX) {
+      const uint32_t s = sa[u] >> shift;
+      acc[0] = mfma_mx<0, 0>(a[u][0], b[u], acc[0], s, sb[u]);
+      if constexpr (RB == 2) acc[1] = mfma_mx<1, 0>(a[u][1], b[u], acc[1], s, sb[u]);
+    } else {
+      acc[0] = mfma16x16x32(a[u][0], b[u], acc[0]);
+      if constexpr (RB == 2) acc[1] = mfma16x16x32(a[u][1], b[u], acc[1]);
+    }
+  }
+};
+
 // ------------------------------------------------------------------ kernel 1
 
 // Partial logits of 16 experts over one range of d by one wavefront: the
@@ -394,19 +423,21 @@ __device__ __forceinline__ void few_lds_barrier() {
   raw_barrier();
 }
 
-// Activation of a GEMM1 task (64 packed rows: 32 intermediate indices gated,
-// 64 ungated) from the four wavefronts' accumulators: gate and up meet in
+// Activation of a GEMM1 task (64 RB packed rows: 32 RB intermediate indices
+// gated, 64 RB ungated) from the four wavefronts' accumulators: gate and up meet in
 // LDS, and 16 consecutive lanes hold one token's block of 32 for the scale.
-template <bool MX, bool GATED>
-__device__ __forceinline__ void few_act(const FewArgs& A, const FewRoute& R, float* h, int slot, int nq, const f32x4& acc) {
+template <bool MX, bool GATED, int RB>
+__device__ __forceinline__ void few_act(const FewArgs& A, const FewRoute& R, float* h, int slot, int nq, const f32x4 (&acc)[RB]) {
   const int lane = lane_id(), r = lane & 15, g = lane >> 4;
   const int base = R.base[slot], m = R.base[slot + 1] - base;
   few_lds_barrier();  // h free
 #pragma unroll
-  for (int i = 0; i < 4; ++i) h[(wave_id() * 16 + 4 * g + i) * kHStride + r] = acc[i];
+  for (int a = 0; a < RB; ++a)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[((wave_id() * RB + a) * 16 + 4 * g + i) * kHStride + r] = acc[a][i];
   few_lds_barrier();
   const int t = threadIdx.x / 16, p = threadIdx.x % 16;  // row of the slot, element pair of a block
-  constexpr int NBLK = GATED ? 1 : 2;
+  constexpr int NBLK = RB * (GATED ? 1 : 2);  // blocks of 32 along I
 #pragma unroll
   for (int blk = 0; blk < NBLK; ++blk) {
     float v[2];
@@ -414,7 +445,7 @@ __device__ __forceinline__ void few_act(const FewArgs& A, const FewRoute& R, flo
     for (int i = 0; i < 2; ++i) {
       const int q = 2 * p + i;  // element of the block
       if constexpr (GATED) {
-        const int hr = (q / 16) * 32 + q % 16;
+        const int hr = blk * 64 + (q / 16) * 32 + q % 16;
         const float h1 = h[hr * kHStride + t], h3 = h[(hr + 16) * kHStride + t];
         v[i] = MX ? mx_silu_mul(h1, h3) : silu_mul(h1, h3);
       } else {
@@ -445,10 +476,10 @@ __device__ __forceinline__ void few_act(const FewArgs& A, const FewRoute& R, flo
   }
 }
 
-// The GEMM1 tasks blockIdx.x, + gridDim.x, ... of n (slot i / per, 64 packed
-// rows i % per), 16 rows a wavefront; the loads run on from one task into the
-// next, as in few_gemm2.
-template <bool MX, bool GATED, int U>
+// The GEMM1 tasks blockIdx.x, + gridDim.x, ... of n (slot i / per, 64 RB packed
+// rows i % per), RB row blocks a wavefront (few_row_blocks).  The loads run on
+// from one task into the next, as in few_gemm2.
+template <bool MX, bool GATED, int RB, int U>
 __device__ __forceinline__ void few_gemm1(const FewArgs& A, const FewRoute& R, float* h, int n, int per) {
   const int lane = lane_id(), r = lane & 15, g = lane >> 4, wave = uniform(wave_id());
   const int N = (GATED ? 2 : 1) * A.I, KB = MX ? A.d / 128 : A.d / 32, step = static_cast<int>(gridDim.x);
@@ -466,48 +497,43 @@ __device__ __forceinline__ void few_gemm1(const FewArgs& A, const FewRoute& R, f
       left = 1 << 30;
       return;
     }
-    const int slot = uniform(li / per), nq = uniform(li % per), nb = nq * 4 + wave;
+    const int slot = uniform(li / per), nb = (uniform(li % per) * 4 + wave) * RB;
     const int e = uniform(R.slot_e[slot]), m = uniform(R.base[slot + 1] - R.base[slot]);
     const int tok = nth_bit(R.mask[e], min(r, m - 1));
     left = KB;
     b = A.xs + (static_cast<size_t>(g) * A.T + tok) * 16;
     if constexpr (MX) {
       w = A.w13 + e * mx_mat_codes(N, A.d) + static_cast<size_t>(nb) * KB * 1024 + lane * 16;
-      ws = A.w13s + e * mx_mat_scales(N, A.d) + static_cast<size_t>(nq) * mx_kq(A.d) * 1024 + lane * 4 + wave;
+      ws = A.w13s + e * mx_mat_scales(N, A.d) + static_cast<size_t>(nb / 4) * mx_kq(A.d) * 1024 + lane * 4;
       bs = A.xs + static_cast<size_t>(A.T) * A.d / 2 + static_cast<size_t>(g) * A.T + tok;
     } else {
       w = A.w13 + (static_cast<size_t>(e) * N * A.d + frag_offset(nb, 0, KB)) * 2 + lane * 16;
     }
   };
-  u32x4 ra[U], rb[U];
-  uint32_t sa[U], sb[U];
+  const size_t w1 = static_cast<size_t>(KB) * 1024;  // to the second row block
+  const int shift = 8 * (wave * RB % 4);             // the wavefront's bytes of a scale word
+  FewRing<MX, RB, U> ring;
   auto load = [&](int u) {
-    ra[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w));
-    rb[u] = ld16(b);
-    if constexpr (MX) {
-      sa[u] = *ws;
-      sb[u] = *bs;
-      ws += on * 256;
-      bs += on * (bstep / 16);
-    }
+    ring.load(u, w, w1, b, ws, bs);
     w += on * 1024;
     b += on * bstep;
+    if (MX) ws += on * 256, bs += on * (bstep / 16);
     if (--left == 0) next();
   };
   next();
 #pragma unroll
   for (int u = 0; u < U; ++u) load(u);
-  f32x4 acc{0.f, 0.f, 0.f, 0.f};
+  f32x4 acc[RB] = {};
   int ci = static_cast<int>(blockIdx.x), todo = KB;
   while (ci < n) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (ci < n) {
-        if constexpr (MX) acc = mfma_mx<0, 0>(ra[u], rb[u], acc, sa[u], sb[u]);
-        else acc = mfma16x16x32(ra[u], rb[u], acc);
+        ring.multiply(u, acc, shift);
         if (--todo == 0) {
-          few_act<MX, GATED>(A, R, h, uniform(ci / per), uniform(ci % per), acc);
-          acc = f32x4{0.f, 0.f, 0.f, 0.f};
+          few_act<MX, GATED, RB>(A, R, h, uniform(ci / per), uniform(ci % per), acc);
+#pragma unroll
+          for (int a = 0; a < RB; ++a) acc[a] = f32x4{0.f, 0.f, 0.f, 0.f};
           ci += step;
           todo = KB;
         }
@@ -517,14 +543,14 @@ __device__ __forceinline__ void few_gemm1(const FewArgs& A, const FewRoute& R, f
   }
 }
 
-// GEMM2 and combine of 16 * nrb output columns for all slots, by NW
-// wavefronts.  A wavefront takes (slot, 16 columns) jobs; its loads run on
+// GEMM2 and combine of 16 RB nrb output columns for all slots, by NW
+// wavefronts.  A wavefront takes (slot, 16 RB columns) jobs; its loads run on
 // from one job into the next, so the short reductions of a narrow layer do
 // not drain the stream.  The pairs' y meet in LDS in fp32, and each output
 // is combine_token's rank-ordered sum.
-template <bool MX, bool OUT_BF16, int NW, int U>
+template <bool MX, bool OUT_BF16, int RB, int NW, int U>
 __device__ __forceinline__ void few_gemm2(const FewArgs& A, const FewRoute& R, float* __restrict__ y, int task, int nrb) {
-  const int lane = lane_id(), r = lane & 15, g = lane >> 4, cols = 16 * nrb;
+  const int lane = lane_id(), r = lane & 15, g = lane >> 4, cols = 16 * RB * nrb;
   const size_t P = R.base[R.nslots];
   const int KB = MX ? A.I / 128 : A.I / 32, njobs = R.nslots * nrb;
   const uint8_t *w = nullptr, *b = nullptr, *ws = nullptr, *bs = nullptr;
@@ -539,7 +565,7 @@ __device__ __forceinline__ void few_gemm2(const FewArgs& A, const FewRoute& R, f
       left = 1 << 30;
       return;
     }
-    const int slot = uniform(ljob / nrb), nb = task * nrb + uniform(ljob % nrb);
+    const int slot = uniform(ljob / nrb), nb = (task * nrb + uniform(ljob % nrb)) * RB;
     const int e = uniform(R.slot_e[slot]), base = uniform(R.base[slot]), m = uniform(R.base[slot + 1]) - base;
     const int rr = min(r, m - 1);
     wstep = 1024;
@@ -547,7 +573,7 @@ __device__ __forceinline__ void few_gemm2(const FewArgs& A, const FewRoute& R, f
     left = KB;
     if constexpr (MX) {
       w = A.w2 + e * mx_mat_codes(A.d, A.I) + static_cast<size_t>(nb) * KB * 1024 + lane * 16;
-      ws = A.w2s + e * mx_mat_scales(A.d, A.I) + static_cast<size_t>(nb / 4) * mx_kq(A.I) * 1024 + lane * 4 + nb % 4;
+      ws = A.w2s + e * mx_mat_scales(A.d, A.I) + static_cast<size_t>(nb / 4) * mx_kq(A.I) * 1024 + lane * 4;
       b = A.act + static_cast<size_t>(base) * A.I / 2 + (static_cast<size_t>(g) * m + rr) * 16;
       bs = A.act + P * A.I / 2 + static_cast<size_t>(base) * (A.I / 32) + static_cast<size_t>(g) * m + rr;
     } else {
@@ -557,17 +583,11 @@ __device__ __forceinline__ void few_gemm2(const FewArgs& A, const FewRoute& R, f
   };
   __syncthreads();  // y free
   if (uniform(wave_id()) < njobs) {
-    u32x4 ra[U], rb[U];
-    uint32_t sa[U], sb[U];
+    const size_t w1 = static_cast<size_t>(KB) * 1024;  // to the second row block
+    FewRing<MX, RB, U> ring;
     auto load = [&](int u) {
-      ra[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w));
-      rb[u] = ld16(b);
-      if constexpr (MX) {
-        sa[u] = *ws;
-        sb[u] = *bs;
-        ws += wstep / 4;
-        bs += bstep / 16;
-      }
+      ring.load(u, w, w1, b, ws, bs);
+      if (MX) ws += wstep / 4, bs += bstep / 16;
       w += wstep;
       b += bstep;
       if (--left == 0) next();
@@ -575,18 +595,23 @@ __device__ __forceinline__ void few_gemm2(const FewArgs& A, const FewRoute& R, f
     next();
 #pragma unroll
     for (int u = 0; u < U; ++u) load(u);
-    f32x4 acc{0.f, 0.f, 0.f, 0.f};
+    f32x4 acc[RB] = {};
     int job = uniform(wave_id()), todo = KB;
     while (job < njobs) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (job < njobs) {
-          if constexpr (MX) acc = mfma_mx<0, 0>(ra[u], rb[u], acc, sa[u], sb[u]);
-          else acc = mfma16x16x32(ra[u], rb[u], acc);
+          const int rb = uniform(job % nrb);
+          ring.multiply(u, acc, 8 * ((task * nrb + rb) * RB % 4));
           if (--todo == 0) {
             const int slot = uniform(job / nrb), base = uniform(R.base[slot]), m = uniform(R.base[slot + 1]) - base;
-            if (r < m) *reinterpret_cast<f32x4*>(y + (base + r) * cols + (job % nrb) * 16 + 4 * g) = acc;
-            acc = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (r < m) {
+              float* yr = y + (base + r) * cols + rb * 16 * RB + 4 * g;
+#pragma unroll
+              for (int a = 0; a < RB; ++a) *reinterpret_cast<f32x4*>(yr + 16 * a) = acc[a];
+            }
+#pragma unroll
+            for (int a = 0; a < RB; ++a) acc[a] = f32x4{0.f, 0.f, 0.f, 0.f};
             job += NW;
             todo = KB;
           }
@@ -613,38 +638,73 @@ __device__ __forceinline__ void few_gemm2(const FewArgs& A, const FewRoute& R, f
   }
 }
 
-template <bool MX, bool GATED>
-__global__ __launch_bounds__(256, 4) void few_gemm1_kernel(FewArgs A) {
+template <bool MX, bool GATED, int RB>
+__global__ __launch_bounds__(256, RB == 2 ? 3 : 4) void few_gemm1_kernel(FewArgs A) {
   extern __shared__ __align__(16) float few_h[];  // the logits, then h
   __shared__ FewRoute R;
   few_route<256, true>(A, R, few_h, blockIdx.x == 0);  // ends with a barrier: the logits are free
-  const int per = (GATED ? 2 : 1) * A.I / 64, n = uniform(R.nslots) * per;
-  few_gemm1<MX, GATED, 8>(A, R, few_h, n, per);
+  const int per = (GATED ? 2 : 1) * A.I / (64 * RB), n = uniform(R.nslots) * per;
+  few_gemm1<MX, GATED, RB, 8>(A, R, few_h, n, per);
 }
 
 constexpr int kFewWaves2 = 8;
 
-// y in LDS: 16 * nrb columns a pair.  nrb is 1 from 8 slots up; with fewer
-// there are at most 16 pairs a slot: 7 * 16 pairs of 32 columns, 3 * 16 of 64
-// or 16 of 128.
-constexpr size_t few_y_bytes(int pairs) { return static_cast<size_t>(pairs * 16 > 3584 ? pairs * 16 : 3584) * 4; }
+// y in LDS: 16 RB nrb columns a pair.  nrb is 1 from 8 slots up; with fewer
+// there are at most 16 pairs a slot: 7 * 16 pairs of 32 RB columns, 3 * 16 of
+// 64 RB, or 16 of 128 (RB = 1).
+constexpr size_t few_y_bytes(int pairs, int rb) { return static_cast<size_t>(pairs * 16 > 3584 ? pairs * 16 : 3584) * 4 * rb; }
 
-template <bool MX, bool OUT_BF16>
-__global__ __launch_bounds__(64 * kFewWaves2, 4) void few_gemm2_kernel(FewArgs A) {
+template <bool MX, bool OUT_BF16, int RB>
+__global__ __launch_bounds__(64 * kFewWaves2, RB == 2 ? 2 : 4) void few_gemm2_kernel(FewArgs A) {
   extern __shared__ __align__(16) float few_y[];
   __shared__ FewRoute R;
   few_route<64 * kFewWaves2, false>(A, R, nullptr, false);
-  // enough jobs for the wavefronts: 1, 2, 4 or 8 column blocks
-  const int ns = uniform(R.nslots), nrb = ns >= 8 ? 1 : (ns >= 4 ? 2 : (ns >= 2 ? 4 : 8)), n = A.d / (16 * nrb);
-  // Workgroups go to the XCDs in turn.  The four row blocks of an MXFP4 scale
+  // enough jobs for the wavefronts
+  const int ns = uniform(R.nslots), nrb = ns >= 8 ? 1 : (ns >= 4 ? 2 : (ns >= 2 || RB == 2 ? 4 : 8));
+  const int n = A.d / (16 * RB * nrb);
+  // Workgroups go to the XCDs in turn.  The G tasks that share an MXFP4 scale
   // word are given to one XCD, one after the other, so that it is fetched
-  // once; in plain order four XCDs fetched it, a fifth of the bytes more.
-  const int quads = nrb == 1 ? n / 32 * 32 : 0;
+  // once; in plain order several XCDs fetched it, a fifth of the bytes more.
+  constexpr int G = 4 / RB;
+  const int shared = nrb == 1 ? n / (8 * G) * (8 * G) : 0;
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
     const int j = i / 8;
-    const int task = i < quads ? (j / 4 * 8 + i % 8) * 4 + j % 4 : i;
-    few_gemm2<MX, OUT_BF16, kFewWaves2, 8>(A, R, few_y, task, nrb);
+    const int task = i < shared ? (j / G * 8 + i % 8) * G + j % G : i;
+    few_gemm2<MX, OUT_BF16, RB, kFewWaves2, 8>(A, R, few_y, task, nrb);
   }
+}
+
+// Row blocks a wavefront multiplies with one token operand (and, in MXFP4,
+// one scale word).  Two where the layer streams: with one, the number of
+// loads bound the 4-bit stream (eight tokens of d = 7168, I = 2048 on 26
+// experts: 85 and 41 us for the two products, with two 74 and 35; the same
+// traffic).  One where a wavefront's latency counts (13 tokens, d = 2048, I =
+// 512: 17.2 and 7.7 us, with two 17.7 and 8.8) and for bf16, which has no
+// scales to load (one token, d = 7168: 75 and 39 us with either; d = 2048, I =
+// 768: 14.8 and 9.6 us, with two 16.9 and 13.7).  The border lies between
+// 35 and 125 MB of first-product weights that the batch can touch.
+int few_row_blocks(const moe_problem_t& p, bool mx, int slots) {  // 2: mx only
+  return mx && static_cast<double>(slots) * gate_rows(p) * p.I * p.d / 2 >= 64e6 ? 2 : 1;
+}
+
+template <int RB>
+hipError_t few_experts(const FewArgs& A, const moe_problem_t& p, bool mx, int slots, hipStream_t s) {
+  const bool gated = gate_rows(p) == 2, obf = p.out_dtype == MOE_BF16;
+  int dev = 0, cus = 0;
+  hipError_t e;
+  if ((e = hipGetDevice(&dev)) != hipSuccess) return e;
+  if ((e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev)) != hipSuccess) return e;
+  const int n1 = slots * (gate_rows(p) * p.I / (64 * RB)), n2 = p.d / (16 * RB);
+  auto g1 = gated ? few_gemm1_kernel<true, true, RB> : few_gemm1_kernel<true, false, RB>;
+  if constexpr (RB == 1)
+    if (!mx) g1 = gated ? few_gemm1_kernel<false, true, RB> : few_gemm1_kernel<false, false, RB>;
+  g1<<<min(n1, (RB == 2 ? 3 : 4) * cus), 256, max(64 * RB * kHStride, p.T * p.E_global) * sizeof(float), s>>>(A);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  auto g2 = obf ? few_gemm2_kernel<true, true, RB> : few_gemm2_kernel<true, false, RB>;
+  if constexpr (RB == 1)
+    if (!mx) g2 = obf ? few_gemm2_kernel<false, true, RB> : few_gemm2_kernel<false, false, RB>;
+  g2<<<min(n2, 2 * cus), 64 * kFewWaves2, few_y_bytes(p.T * min(p.k, p.E_local), RB), s>>>(A);
+  return hipGetLastError();
 }
 
 template <bool XBF, bool MX>
@@ -661,7 +721,7 @@ hipError_t launch_forward_few(const moe_problem_t& p, const WsLayout& L, const v
                               const float* bias, int32_t* topk_idx, float* topk_w, float* logits, void* out, char* ws,
                               hipStream_t s) {
   if (p.T == 0) return hipSuccess;
-  const bool xbf = p.x_dtype == MOE_BF16, gated = gate_rows(p) == 2, obf = p.out_dtype == MOE_BF16;
+  const bool xbf = p.x_dtype == MOE_BF16;
   const uint8_t* base = static_cast<const uint8_t*>(packed);
   FewArgs A{};
   A.x = x;
@@ -696,20 +756,8 @@ hipError_t launch_forward_few(const moe_problem_t& p, const WsLayout& L, const v
   hipError_t e = xbf ? (mx ? front<true, true>(A, s) : front<true, false>(A, s))
                      : (mx ? front<false, true>(A, s) : front<false, false>(A, s));
   if (e != hipSuccess) return e;
-  int dev = 0, cus = 0;
-  if ((e = hipGetDevice(&dev)) != hipSuccess) return e;
-  if ((e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev)) != hipSuccess) return e;
-  // most slots a batch can touch
-  const int slots = min(p.E_local, p.T * p.k);
-  const int n1 = slots * (gate_rows(p) * p.I / 64), n2 = p.d / 16;
-  auto g1 = mx ? (gated ? few_gemm1_kernel<true, true> : few_gemm1_kernel<true, false>)
-               : (gated ? few_gemm1_kernel<false, true> : few_gemm1_kernel<false, false>);
-  g1<<<min(n1, 4 * cus), 256, max(64 * kHStride, p.T * p.E_global) * sizeof(float), s>>>(A);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  auto g2 = mx ? (obf ? few_gemm2_kernel<true, true> : few_gemm2_kernel<true, false>)
-               : (obf ? few_gemm2_kernel<false, true> : few_gemm2_kernel<false, false>);
-  g2<<<min(n2, 2 * cus), 64 * kFewWaves2, few_y_bytes(p.T * min(p.k, p.E_local)), s>>>(A);
-  return hipGetLastError();
+  const int slots = min(p.E_local, p.T * p.k);  // most experts the batch can touch
+  return few_row_blocks(p, mx, slots) == 2 ? few_experts<2>(A, p, mx, slots, s) : few_experts<1>(A, p, mx, slots, s);
 }
 
 }  // namespace moe

@@ -76,6 +76,7 @@ CASES = [  # T, d, I, E, k, E_local, e_begin
     (16, 256, 256, 4, 4, 4, 0), (15, 1152, 640, 33, 6, 33, 0), (8, 512, 512, 65, 8, 65, 0), (5, 768, 128, 200, 12, 40, 80),
     (13, 2048, 512, 128, 6, 32, 0), (16, 1024, 256, 256, 8, 256, 0), (16, 128, 128, 64, 64, 64, 0), (7, 256, 128, 16, 1, 1, 15),
     (1, 7168, 2048, 32, 8, 32, 0),
+    (16, 2176, 640, 80, 8, 80, 0), (9, 2048, 1024, 64, 3, 64, 0),   # two row blocks a wavefront in MXFP4
 ]
 
 
@@ -147,6 +148,111 @@ def test_batch_invariance(mx):
         torch.cuda.synchronize()
         for n in ("idx", "w", "out"):
             assert torch.equal(one[n][0], whole[n][t])
+
+
+@pytest.mark.parametrize("act", [GATED, UNGATED])
+def test_batch_invariance_across_wavefront_tiles(act):
+    """16 tokens run two row blocks a wavefront, one token runs one."""
+    print(f"[case] few tiles act={act}", flush=True)
+    L = Few(16, 2048, 1152, 64, 8, act=act, mx=True)
+    whole = L.check()
+    for t in (0, 9):
+        one = moe.forward_few(L.p.replace(T=1), L.x[t:t + 1].contiguous(), L.packed, L.ws, mxfp4=True)
+        torch.cuda.synchronize()
+        for n in ("idx", "w", "out"):
+            assert torch.equal(one[n][0], whole[n][t])
+
+
+def _graph(step, outs):
+    """Four replays, each over poisoned outputs and followed by an eager step
+    on the same workspace, give the eager step's bits."""
+    step()
+    torch.cuda.synchronize()
+    want = [o.clone() for o in outs()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    captured = outs()
+    torch.cuda.synchronize()
+    for rep in range(4):
+        for o in captured:
+            o.view(torch.uint8).fill_(0x7F)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(captured, want):
+            assert torch.equal(o, w), rep
+        step()
+        torch.cuda.synchronize()
+        for o, w in zip(outs(), want):
+            assert torch.equal(o, w), rep
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_graph_replays(mx):
+    print(f"[case] few graph mx={mx}", flush=True)
+    L = Few(5, 512, 256, 16, 4, mx=mx)
+    got = {}
+
+    def step():
+        got.update(moe.forward_few(L.p, L.x, L.packed, L.ws, mxfp4=mx))
+
+    _graph(step, lambda: [got["idx"], got["w"], got["out"]])
+
+
+@pytest.mark.parametrize("T", [7, 300])
+def test_graph_replays_of_the_mxfp4_layer(T):
+    """route, dispatch, quantise, expert FFN: the streaming and the wide tiles."""
+    print(f"[case] mxfp4 graph T={T}", flush=True)
+    L = Few(T, 512, 256, 3, 2, mx=True)
+    got = {}
+
+    def step():
+        got.update(moe.forward_mxfp4(L.p, L.x, L.packed, L.ws))
+
+    _graph(step, lambda: [got["idx"], got["w"], got["out"]])
+
+
+def test_on_another_stream_and_twice_on_one_workspace():
+    """The calls follow the current stream; a second call on the workspace in
+    the same stream finds nothing of the first."""
+    print("[case] few streams", flush=True)
+    A, B = Few(3, 512, 256, 16, 4, seed=1), Few(16, 256, 128, 8, 2, mx=True, seed=2)
+    ra, rb = A.check(), B.check()
+    n = max(moe.workspace_size(A.p), moe.workspace_size(B.p))
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = []
+        for _ in range(5):
+            got.append((moe.forward_few(A.p, A.x, A.packed, ws), moe.forward_few(B.p, B.x, B.packed, ws, mxfp4=True)))
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert torch.equal(a["out"], ra["out"]) and torch.equal(b["out"], rb["out"])
+
+
+def test_refused_tensors():
+    L = Few(4, 256, 128, 8, 2)
+    with pytest.raises(ValueError, match="not contiguous"):
+        moe.forward_few(L.p, L.x.t().contiguous().t(), L.packed, L.ws)
+    with pytest.raises(ValueError, match="packed"):
+        moe.forward_few(L.p, L.x, L.packed, L.ws, mxfp4=True)      # the other format's buffer
+    with pytest.raises(moe.MoEError) as e:
+        moe.forward_few(L.p, L.x, L.packed, L.ws[:1024])
+    assert e.value.status == moe.MOE_ERR_WORKSPACE
+    with pytest.raises(moe.MoEError) as e:
+        off = torch.empty(4 * 256 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(4, 256)
+        moe.forward_few(L.p, off, L.packed, L.ws)
+    assert e.value.status == moe.MOE_ERR_INVALID_ARG
+    with pytest.raises(ValueError, match="bias"):
+        moe.forward_few(L.p, L.x, L.packed, L.ws, bias=torch.zeros(8, dtype=torch.float64, device="cuda"))
 
 
 def test_no_tokens_and_too_many():
