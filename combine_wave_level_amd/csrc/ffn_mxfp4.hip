@@ -186,23 +186,26 @@ __device__ __forceinline__ void mx_tiles(const MxArgs& A, int NT, F f) {
 }
 
 // MxWide's token operand: the codes and scales of the routed rows in sorted
-// order, in fragment layout over the padded rows.  Workgroup b: row blocks
-// b, b + grid, ... (their codes), and the scale words of whole quads.  The
-// rows are in the caches (a token row is read about k times); 1 KiB runs are
-// written.  Rows that pad an expert repeat its last row.
+// order, in fragment layout over the padded rows (rows that pad an expert
+// repeat its last one).  A workgroup takes 64 rows and a range of four-step
+// groups of K: a wavefront copies a row block's pieces of a fragment (16 rows
+// of 64 bytes, from the caches; 1 KiB written), and the scales pass through
+// LDS, 16 bytes of a row at a time, on their way into words (fetched word by
+// word they touched as many lines again as the codes).
 __global__ __launch_bounds__(256) void mx_gather_kernel(const uint8_t* __restrict__ xc, const uint8_t* __restrict__ xs,
                                                         const int32_t* __restrict__ offsets,
                                                         const int32_t* __restrict__ sorted_token, int E_local, int K,
                                                         uint8_t* __restrict__ fc, uint8_t* __restrict__ fs) {
   __shared__ int32_t seg[kMaxLocalExperts + 1];
   __shared__ int32_t tok[64];
+  __shared__ __align__(16) uint8_t sc[64 * 16];
   mx_seg_prefix(offsets, E_local, seg);
   __syncthreads();
   const int nquads = uniform(seg[E_local]), KB = K / 128, kq = mx_kq(K);
   const size_t cs = mx_codes_stride(K), ss = mx_scales_stride(K);
-  // this workgroup's K steps
-  const int k0 = static_cast<int>(static_cast<long long>(KB) * blockIdx.y / gridDim.y);
-  const int nk = static_cast<int>(static_cast<long long>(KB) * (blockIdx.y + 1) / gridDim.y) - k0;
+  const int g0 = kq * static_cast<int>(blockIdx.y) / static_cast<int>(gridDim.y);
+  const int g1 = kq * (static_cast<int>(blockIdx.y) + 1) / static_cast<int>(gridDim.y);
+  const int l = lane_id(), rb = wave_id();
   for (int q = blockIdx.x; q < nquads; q += gridDim.x) {
     const int e = uniform(sched_expert_of(seg, 0, E_local, q));
     __syncthreads();  // tok free
@@ -211,20 +214,25 @@ __global__ __launch_bounds__(256) void mx_gather_kernel(const uint8_t* __restric
       tok[threadIdx.x] = sorted_token[min(r, offsets[e + 1] - 1)];
     }
     __syncthreads();
-    // a wavefront a row block: its lanes' pieces of the fragments, four at a time
-    const int l = lane_id(), rb = wave_id();
-    const uint8_t* src = xc + static_cast<size_t>(tok[rb * 16 + l % 16]) * cs + k0 * 64 + (l / 16) * 16;
-    uint8_t* dst = fc + (static_cast<size_t>(q * 4 + rb) * KB + k0) * 1024 + l * 16;
-#pragma unroll 4
-    for (int k = 0; k < nk; ++k) st16(dst + k * 1024, ld16(src + k * 64));
-    for (int i = threadIdx.x; i < nk * 64; i += 256) {
-      const int w = i % 64, ks = k0 + i / 64;
-      uint32_t v = 0;
+    const uint8_t* src = xc + static_cast<size_t>(tok[rb * 16 + l % 16]) * cs + (l / 16) * 16;
+    uint8_t* dst = fc + static_cast<size_t>(q * 4 + rb) * KB * 1024 + l * 16;
+    for (int g = g0; g < g1; ++g) {
+      u32x4 v[4];
 #pragma unroll
-      for (int a = 0; a < 4; ++a)
-        v |= (*reinterpret_cast<const uint32_t*>(xs + static_cast<size_t>(tok[a * 16 + w % 16]) * ss + ks * 4) >>
-              (8 * (w / 16)) & 255u) << (8 * a);
-      *reinterpret_cast<uint32_t*>(fs + (static_cast<size_t>(q) * kq * 4 + ks) * 256 + w * 4) = v;
+      for (int k = 0; k < 4; ++k)
+        if (g * 4 + k < KB) v[k] = ld16(src + (g * 4 + k) * 64);
+      if (threadIdx.x < 64)
+        st16(sc + threadIdx.x * 16, ld16(xs + static_cast<size_t>(tok[threadIdx.x]) * ss + g * 16));
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (g * 4 + k < KB) st16(dst + static_cast<size_t>(g * 4 + k) * 1024, v[k]);
+      __syncthreads();
+      // word (step rb of the group, lane l); steps past K are never read
+      uint32_t w = 0;
+#pragma unroll
+      for (int a = 0; a < 4; ++a) w |= static_cast<uint32_t>(sc[(a * 16 + l % 16) * 16 + rb * 4 + l / 16]) << (8 * a);
+      *reinterpret_cast<uint32_t*>(fs + (static_cast<size_t>(q) * kq + g) * 1024 + rb * 256 + l * 4) = w;
+      __syncthreads();
     }
   }
 }
@@ -339,7 +347,7 @@ hipError_t launch_ffn_mxfp4(const moe_problem_t& p, const WsLayout& L, const uin
   } else {
     uint8_t* fc = static_cast<uint8_t*>(y);
     uint8_t* fs = fc + (pad + 64) * (p.d / 2);
-    const dim3 ggrid(static_cast<unsigned>(min(pad / 64, static_cast<size_t>(2048))), min(p.d / 128, 8));
+    const dim3 ggrid(static_cast<unsigned>(min(pad / 64, static_cast<size_t>(2048))), min(mx_kq(p.d), 8));
     mx_gather_kernel<<<ggrid, 256, 0, s>>>(
         xc, xs, offsets, sorted_token, p.E_local, p.d, fc, fs);
     if ((e = hipGetLastError()) != hipSuccess) return e;
