@@ -238,7 +238,7 @@ __global__ __launch_bounds__(256) void mx_gather_kernel(const uint8_t* __restric
 }
 
 template <class C, bool GATED>
-__global__ __launch_bounds__(C::NTHREADS, C::STREAM ? 3 : 4) void gemm1_mx_kernel(MxArgs A) {
+__global__ __launch_bounds__(C::NTHREADS, C::PER_CU * C::NW / 4) void gemm1_mx_kernel(MxArgs A) {
   extern __shared__ __align__(16) uint8_t mx_lds[];
   const int N = (GATED ? 2 : 1) * A.I;
   mx_tiles<C>(A, N / C::BW, [&](int e, int row0, int count, int nt, int prow0) {
@@ -257,7 +257,7 @@ __global__ __launch_bounds__(C::NTHREADS, C::STREAM ? 3 : 4) void gemm1_mx_kerne
 }
 
 template <class C>
-__global__ __launch_bounds__(C::NTHREADS, C::STREAM ? 3 : 4) void gemm2_mx_kernel(MxArgs A) {
+__global__ __launch_bounds__(C::NTHREADS, C::PER_CU * C::NW / 4) void gemm2_mx_kernel(MxArgs A) {
   extern __shared__ __align__(16) uint8_t mx_lds[];
   static_assert(static_cast<size_t>(C::BT) * C::BW * 2 <= C::LDS_BYTES, "output stage fits the tile's LDS");
   mx_tiles<C>(A, A.d / C::BW, [&](int e, int row0, int count, int nt, int prow0) {
@@ -294,24 +294,25 @@ __global__ __launch_bounds__(C::NTHREADS, C::STREAM ? 3 : 4) void gemm2_mx_kerne
   });
 }
 
-template <class K>
-hipError_t launch_phase(K kern, int threads, size_t lds, const MxArgs& A, hipStream_t s) {
-  int dev = 0, cus = 0, per_cu = 0;
+// The grid is what the device holds at once (LDS and registers of both
+// products' kernels fit C::PER_CU workgroups a CU by their bounds).
+template <class C, class K>
+hipError_t launch_phase(K kern, const MxArgs& A, hipStream_t s) {
+  int dev = 0, cus = 0;
   hipError_t e;
   if ((e = hipGetDevice(&dev)) != hipSuccess) return e;
   if ((e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev)) != hipSuccess) return e;
-  if ((e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, kern, threads, lds)) != hipSuccess) return e;
-  kern<<<max(1, per_cu) * cus, threads, lds, s>>>(A);
+  kern<<<C::PER_CU * cus, C::NTHREADS, C::LDS_BYTES, s>>>(A);
   return hipGetLastError();
 }
 
 template <class C>
 hipError_t launch_g1(bool gated, const MxArgs& A, hipStream_t s) {
-  return launch_phase(gated ? gemm1_mx_kernel<C, true> : gemm1_mx_kernel<C, false>, C::NTHREADS, C::LDS_BYTES, A, s);
+  return launch_phase<C>(gated ? gemm1_mx_kernel<C, true> : gemm1_mx_kernel<C, false>, A, s);
 }
 template <class C>
 hipError_t launch_g2(const MxArgs& A, hipStream_t s) {
-  return launch_phase(gemm2_mx_kernel<C>, C::NTHREADS, C::LDS_BYTES, A, s);
+  return launch_phase<C>(gemm2_mx_kernel<C>, A, s);
 }
 
 }  // namespace
@@ -324,18 +325,22 @@ hipError_t launch_ffn_mxfp4(const moe_problem_t& p, const WsLayout& L, const uin
   const int gr = gate_rows(p);
   const PackedMxLayout PL = packed_mx_layout(p.d, p.I, p.E_global, p.E_local, p.x_dtype == MOE_BF16, gr);
   const uint8_t* base = static_cast<const uint8_t*>(packed);
-  // 96 rows an expert and more: the matrix-bound tiles, where their operands
-  // fit.  The activations in 4 bits take the place of the bf16 ones (2 I
-  // bytes a row of P_max).  MxStream: rows of at most I / 2 + 64 code and
-  // I / 32 + 12 scale bytes.  MxWide: fragments over the padded rows (and the
-  // 64 rows that the last tile may read past them), and the gathered
-  // token operand likewise in the place of y (2 d bytes a row), which the
-  // second product then writes: with P_max >= 96 E_local that takes about half
-  // of either, and only layers a few hundred wide with one or two experts
-  // fall short.
+  // The matrix-bound tiles from 64 rows an expert on the average.  Measured,
+  // quantisation to combine, MxWide against MxStream: d = 4096, I = 1024, 16
+  // experts: 49 against 40 us at 48 rows, 53.5 against 54.4 at 64, 58 against
+  // 60 at 96; d = 7168, I = 2048, 32 experts: 179 against 173, 190 against
+  // 251, 206 against 340; d = 2048, I = 768, 64 experts: 63 against 53, 69
+  // against 74, 76 against 89.  And where their operands fit: the activations
+  // in 4 bits take the place of the bf16 ones (2 I bytes a row of P_max).
+  // MxStream: rows of at most I / 2 + 64 code and I / 32 + 12 scale bytes.
+  // MxWide: fragments over the padded rows (and the up to 64 rows that the
+  // last tile may read past them), and the gathered token operand likewise in
+  // the place of y (2 d bytes a row), which the second product then writes:
+  // with P_max >= 64 E_local that takes a little over half of either, and
+  // only layers a few hundred wide with one or two experts fall short.
   const size_t pad = static_cast<size_t>(L.P_pad), pmax = static_cast<size_t>(L.P_max);
   const auto frag_bytes = [&](int K) { return (pad + 64) * (static_cast<size_t>(K) / 2 + 16 * static_cast<size_t>(mx_kq(K))); };
-  const bool wide = static_cast<double>(p.T) * p.k / p.E_global >= 96.0 && frag_bytes(p.d) <= pmax * p.d * 2 &&
+  const bool wide = static_cast<double>(p.T) * p.k / p.E_global >= 64.0 && frag_bytes(p.d) <= pmax * p.d * 2 &&
                     frag_bytes(p.I) <= pmax * p.I * 2;
   uint8_t* ac = reinterpret_cast<uint8_t*>(ws + L.act);
   MxArgs A{xc, xs, base + PL.w13, base + PL.w13s, offsets, sorted_token, ac,

@@ -24,7 +24,11 @@
 //   gathers them, do not fit LDS far enough ahead.  A 256 x 256 tile with one
 //   workgroup a CU moves a third fewer bytes, but a CU had nothing to
 //   multiply while it started or ended a tile, and 2.25 such tiles a CU (16
-//   experts of about 1024 rows, 2048 weight rows) take the time of three.
+//   experts of about 1024 rows, 2048 weight rows) take the time of three
+//   (that layer's two products: 165 and 90 us with token lines, 129 and 82
+//   with fragments, 95 and 73 with this tile; 4 wavefronts of 128 x 64 in its
+//   place 105 and 74).  What binds it: 102 KiB of loads in flight a CU
+//   against two to three microseconds until they arrive.
 // MxStream (a few rows an expert, bound by the weights' bytes): 128 x 64, 4
 //   wavefronts of 64 x 32, token rows gathered by the tile, all operands in 4
 //   stages of one K step; three workgroups a CU, so that some load while
@@ -54,6 +58,7 @@ __device__ __forceinline__ void lds_dma4(const void* g, void* l) { __builtin_amd
 template <int BW_>
 struct MxWide {
   static constexpr bool STREAM = false;
+  static constexpr int PER_CU = 2;  // workgroups
   static constexpr int BW = BW_, BT = 128, WR = BW / 64, WT = 8 / WR, NW = 8, NTHREADS = 512;
   static constexpr int AW = BW / WR / 16, AT = BT / WT / 16;
   static constexpr int NST = 3, LW = BW / 16 / NW, LT = BT / 16 / NW, LS = 1;
@@ -61,11 +66,12 @@ struct MxWide {
   static constexpr int T0 = BW * 64, S0 = T0 + BT * 64, STAGE = S0 + (NQ + NQT) * 256;
   static constexpr size_t LDS_BYTES = static_cast<size_t>(NST) * STAGE;
   static_assert(AW == 4 && (AT == 4 || AT == 2) && LW >= 1 && LT >= 1 && NQ + NQT <= NW, "wave tile, loads");
-  static_assert(2 * (LDS_BYTES + 2304) <= 160 * 1024, "two workgroups a CU, with their tables");
+  static_assert(PER_CU * (LDS_BYTES + 2304) <= 160 * 1024, "two workgroups a CU, with their tables");
 };
 
 struct MxStream {
   static constexpr bool STREAM = true;
+  static constexpr int PER_CU = 3;
   static constexpr int BW = 128, BT = 64, WR = 2, WT = 2, NW = 4, NTHREADS = 256;
   static constexpr int AW = BW / WR / 16, AT = BT / WT / 16;
   static constexpr int NST = 4, LW = BW / 16 / NW, LT = BT / 16 / NW;
@@ -75,7 +81,7 @@ struct MxStream {
   static constexpr size_t LDS_BYTES = static_cast<size_t>(NST) * STAGE;
   static_assert(NQ == 2 && BT == 64 && NW == 4, "one scale load a wavefront and step");
   static_assert((NST - 2) * (LW + LT + LS) <= 63, "vmcnt");
-  static_assert(3 * (LDS_BYTES + 1280) <= 160 * 1024, "three workgroups a CU, with their tables");
+  static_assert(PER_CU * (LDS_BYTES + 1280) <= 160 * 1024, "three workgroups a CU, with their tables");
 };
 
 // wave-uniform, kept in scalar registers

@@ -141,7 +141,8 @@ def _check(status: int, where: str) -> None:
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    # a plain integer: ctypes makes the void pointer
+    return None if t is None else t.data_ptr()
 
 
 def _stream():

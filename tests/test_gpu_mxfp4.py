@@ -265,6 +265,8 @@ FFN = [  # T, d, I, E, k, E_local, x, act
     (600, 640, 128, 3, 2, 3, "f32", 0),
     (513, 896, 640, 4, 4, 2, "bf16", 0),      # a share
     (1100, 1024, 512, 4, 2, 4, "bf16", 0),
+    (100, 128, 128, 1, 1, 1, "bf16", 0),      # many rows, but y has no room for the gathered operand
+    (130, 512, 256, 4, 2, 4, "bf16", 1), (128, 512, 256, 4, 2, 4, "bf16", 0),   # the border between the tiles
 ]
 
 
@@ -302,3 +304,76 @@ def test_a_token_is_the_same_in_any_batch(d, I, act):
     torch.cuda.synchronize()
     assert torch.equal(outs[40], outs[700][330:370])
     assert torch.equal(outs[1], outs[700][350:351])
+
+
+def test_no_rows_and_no_local_rows():
+    L = _layer(5, 256, 128, 8, 2, E_local=2, seed=3)
+    p = L["p"]
+    disp, w_d = _routing(L, np.tile([5, 7], (5, 1)), np.full((5, 2), 0.5))
+    codes, scales = moe.quantize_mxfp4(p, L["x"])
+    out = torch.full((5, 256), float("nan"), dtype=torch.bfloat16, device="cuda")
+    moe.ffn_mxfp4(p, codes, scales, L["packed"], disp, w_d, L["ws"], out=out)
+    assert (out == 0).all()
+    q = p.replace(T=0)
+    ws = moe.workspace(q)
+    disp = moe.dispatch(q, torch.empty(0, 2, dtype=torch.int32, device="cuda"), ws)
+    e = torch.empty(0, 128, dtype=torch.uint8, device="cuda")
+    y, out = moe.ffn_mxfp4(q, e, e[:, :16].contiguous(), L["packed"], disp,
+                           torch.empty(0, 2, device="cuda"), ws)
+    assert out.shape == (0, 256)
+
+
+def test_all_rows_on_one_expert():
+    """Every token picks the same expert of many: more m-tiles than the mean suggests."""
+    print("[case] mxfp4 ffn hot expert", flush=True)
+    L = _layer(333, 512, 256, 16, 1, seed=9)
+    idx, w = np.full((333, 1), 11, np.int32), np.ones((333, 1), np.float32)
+    disp, w_d = _routing(L, idx, w)
+    codes, scales = moe.quantize_mxfp4(L["p"], L["x"])
+    out = moe.ffn_mxfp4(L["p"], codes, scales, L["packed"], disp, w_d, L["ws"])[1]
+    torch.cuda.synchronize()
+    _check_out(L, idx, w, out, np.r_[0, 63, 64, 127, 200, 332])
+
+
+def test_rows_that_are_not_finite_stay_their_own():
+    print("[case] mxfp4 ffn nan", flush=True)
+    for T in (9, 300):
+        L = _layer(T, 256, 128, 4, 2, seed=4)
+        idx, w = _random_routing(L)
+        disp, w_d = _routing(L, idx, w)
+
+        def run():
+            codes, scales = moe.quantize_mxfp4(L["p"], L["x"])
+            return moe.ffn_mxfp4(L["p"], codes, scales, L["packed"], disp, w_d, L["ws"])[1].clone()
+
+        clean = run()
+        L["x"][3, 40] = float("nan")
+        L["x"][7, 200] = float("inf")
+        bad = run()
+        torch.cuda.synchronize()
+        keep = [t for t in range(T) if t not in (3, 7)]
+        assert torch.equal(bad[keep], clean[keep])
+        assert bool(torch.isnan(bad[3]).all()) and bool(torch.isnan(bad[7]).all())
+
+
+def test_quantised_weights_through_the_bf16_path():
+    """What a layer trained on the 4-bit weights runs: unpacked values, packed
+    for bf16, give the float64 layer on those values within the bf16 path's
+    row tolerance (2e-2), and its gradients are finite."""
+    print("[case] mxfp4 weights, bf16 layer", flush=True)
+    L = _layer(48, 256, 128, 4, 2, seed=6)
+    p = L["p"]
+    W1, W3, W2 = moe.unpack_weights_mxfp4(p, L["packed"])
+    for got, src in ((W1, L["W1"]), (W3, L["W3"]), (W2, L["W2"])):
+        assert _same(got.float().cpu().numpy().astype(np.float64), _grid(src, 1))
+    packed, packed_bwd = moe.pack_weights(p, L["Wg"], W1, W3, W2), moe.pack_weights_bwd(p, L["Wg"], W1, W3, W2)
+    ws = moe.workspace(p, backward=True)
+    r = moe.forward(p, L["x"], packed, ws)
+    g = moe.backward(p, L["x"], packed, packed_bwd, r["idx"], r["w"], r["disp"], r["out"], ws, want_dw=True)
+    torch.cuda.synchronize()
+    assert all(bool(torch.isfinite(g[n]).all()) for n in ("dx", "dWg", "dW1", "dW3", "dW2"))
+    idx, w = r["idx"].cpu().numpy(), r["w"].cpu().numpy().astype(np.float64)
+    ref = oracle.forward_tokens(L["xr"].double().numpy(), idx, w, _grid(L["W1"], 1), _grid(L["W3"], 1),
+                                _grid(L["W2"], 1), 0, 4)
+    err = np.abs(r["out"].float().cpu().numpy() - ref).max(1) / np.abs(ref).max(1)
+    assert err.max() <= 2e-2
