@@ -202,34 +202,49 @@ PackedMxLayout layout_of(const moe_problem_t& p) {
   return packed_mx_layout(p.d, p.I, p.E_global, p.E_local, p.x_dtype == MOE_BF16, gate_rows(p));
 }
 
+// f(first row, chunks of eight elements, workgroups) for the rows of a launch:
+// all of them, but for more than 2^34 elements (a launch has fewer than 2^32
+// threads).
+template <class F>
+hipError_t by_rows(int T, int cpr, F f) {
+  const int rows = static_cast<int>(min(size_t{1} << 24, (size_t{1} << 31) / cpr));
+  for (int t = 0; t < T; t += rows) {
+    const size_t n = static_cast<size_t>(min(rows, T - t)) * cpr;
+    f(static_cast<size_t>(t), n, static_cast<unsigned>((n + 255) / 256));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 }  // namespace
 
 hipError_t launch_quantize_mxfp4(const moe_problem_t& p, const void* x, uint8_t* codes, uint8_t* scales,
                                  hipStream_t s) {
-  if (p.T == 0) return hipSuccess;
   const int cpr = p.d / 8;
-  const size_t n = static_cast<size_t>(p.T) * cpr;
-  const unsigned blocks = static_cast<unsigned>((n + 255) / 256);
   const size_t cs = mx_codes_stride(p.d), ss = mx_scales_stride(p.d);
-  if (p.x_dtype == MOE_BF16)
-    quantize_mxfp4_kernel<true><<<blocks, 256, 0, s>>>(x, n, cpr, cs, ss, codes, scales);
-  else
-    quantize_mxfp4_kernel<false><<<blocks, 256, 0, s>>>(x, n, cpr, cs, ss, codes, scales);
-  return hipGetLastError();
+  const size_t row = static_cast<size_t>(p.d) * (p.x_dtype == MOE_BF16 ? 2 : 4);
+  return by_rows(p.T, cpr, [&](size_t t0, size_t n, unsigned blocks) {
+    const void* xr = static_cast<const uint8_t*>(x) + t0 * row;
+    if (p.x_dtype == MOE_BF16)
+      quantize_mxfp4_kernel<true><<<blocks, 256, 0, s>>>(xr, n, cpr, cs, ss, codes + t0 * cs, scales + t0 * ss);
+    else
+      quantize_mxfp4_kernel<false><<<blocks, 256, 0, s>>>(xr, n, cpr, cs, ss, codes + t0 * cs, scales + t0 * ss);
+  });
 }
 
 hipError_t launch_dequantize_mxfp4(const moe_problem_t& p, const uint8_t* codes, const uint8_t* scales, void* x,
                                    hipStream_t s) {
-  if (p.T == 0) return hipSuccess;
   const int cpr = p.d / 8;
-  const size_t n = static_cast<size_t>(p.T) * cpr;
-  const unsigned blocks = static_cast<unsigned>((n + 255) / 256);
   const size_t cs = mx_codes_stride(p.d), ss = mx_scales_stride(p.d);
-  if (p.x_dtype == MOE_BF16)
-    dequantize_mxfp4_kernel<true><<<blocks, 256, 0, s>>>(codes, scales, n, cpr, cs, ss, x);
-  else
-    dequantize_mxfp4_kernel<false><<<blocks, 256, 0, s>>>(codes, scales, n, cpr, cs, ss, x);
-  return hipGetLastError();
+  const size_t row = static_cast<size_t>(p.d) * (p.x_dtype == MOE_BF16 ? 2 : 4);
+  return by_rows(p.T, cpr, [&](size_t t0, size_t n, unsigned blocks) {
+    void* xr = static_cast<uint8_t*>(x) + t0 * row;
+    if (p.x_dtype == MOE_BF16)
+      dequantize_mxfp4_kernel<true><<<blocks, 256, 0, s>>>(codes + t0 * cs, scales + t0 * ss, n, cpr, cs, ss, xr);
+    else
+      dequantize_mxfp4_kernel<false><<<blocks, 256, 0, s>>>(codes + t0 * cs, scales + t0 * ss, n, cpr, cs, ss, xr);
+  });
 }
 
 hipError_t launch_pack_mxfp4(const moe_problem_t& p, const void* Wg, const void* W1, const void* W3, const void* W2,

@@ -86,6 +86,31 @@ def test_crafted_blocks(dt):
     _check_rows(x.astype(np.float32), dt)
 
 
+def test_rows_past_two_to_the_35_elements():
+    """More elements than one launch has threads for: the rows at both ends
+    and around the border between launches are those of a small call."""
+    T, d = (1 << 24) - 3, 2176
+    if torch.cuda.mem_get_info()[0] < 130 << 30:
+        pytest.skip("needs 130 GiB of free memory")
+    print(f"[case] mxfp4 rows T={T} d={d}", flush=True)
+    p, border = _problem(T=T, d=d), (1 << 34) // d
+    at = torch.tensor([0, 1, border - 1, border, border + 1, T - 2, T - 1], device="cuda")
+    rows = torch.randn(len(at), d, generator=torch.Generator("cuda").manual_seed(5), device="cuda").bfloat16()
+    x = torch.zeros(T, d, dtype=torch.bfloat16, device="cuda")
+    x[at] = rows
+    codes, scales = moe.quantize_mxfp4(p, x)
+    del x
+    small = p.replace(T=len(at))
+    c, s = moe.quantize_mxfp4(small, rows)
+    assert torch.equal(codes[at], c) and torch.equal(scales[at], s)
+    back = moe.dequantize_mxfp4(p, codes, scales)
+    assert torch.equal(back[at], moe.dequantize_mxfp4(small, c, s))
+    rest = torch.tensor([2, border // 2, border + 2, T - 3], device="cuda")
+    assert not back[rest].any() and not codes[rest].any()
+    del back, codes, scales
+    torch.cuda.empty_cache()
+
+
 def test_no_rows():
     p = _problem(T=0)
     codes, scales = moe.quantize_mxfp4(p, torch.empty(0, 256, dtype=torch.bfloat16, device="cuda"))
