@@ -19,7 +19,6 @@
 #include "ffn_parts.h"
 #include "moe_internal.h"
 #include "mxfp4.h"
-#include "route_topk.h"
 
 namespace moe {
 namespace {
@@ -48,25 +47,16 @@ struct FewArgs {
 
 // ------------------------------------------------------------------ the stream
 
-// One wavefront: 16 weight rows times the slot's tokens over the whole K.
-// w: the row block's fragments for this lane (1 KiB apart); b: this lane's
-// piece of the token operand, bstep bytes apart (a row past the slot's rows
-// repeats a valid one: its column is not used); MX: ws, bs the scale bytes,
-// 256 and bsstep bytes apart.  U fragments are in flight.
-template <bool MX, int U>
-__device__ __forceinline__ f32x4 few_stream(const uint8_t* __restrict__ w, const uint8_t* __restrict__ b, size_t bstep,
-                                            const uint8_t* __restrict__ ws, const uint8_t* __restrict__ bs,
-                                            size_t bsstep, int n) {
+// One wavefront: 16 rows of router weights times the tokens over n K steps of
+// 32.  w, b: the rows' fragments and the tokens for this lane, 1 KiB and 64
+// bytes apart.  U fragments are in flight.
+template <int U>
+__device__ __forceinline__ f32x4 few_stream(const uint8_t* __restrict__ w, const uint8_t* __restrict__ b, int n) {
   u32x4 ra[U], rb[U];
-  uint32_t sa[U], sb[U];
   auto load = [&](int u, int i) {
     i = min(i, n - 1);
     ra[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w + static_cast<size_t>(i) * 1024));
-    rb[u] = ld16(b + static_cast<size_t>(i) * bstep);
-    if constexpr (MX) {
-      sa[u] = ws[static_cast<size_t>(i) * 256];
-      sb[u] = bs[static_cast<size_t>(i) * bsstep];
-    }
+    rb[u] = ld16(b + static_cast<size_t>(i) * 64);
   };
 #pragma unroll
   for (int u = 0; u < U; ++u) load(u, u);
@@ -74,10 +64,7 @@ __device__ __forceinline__ f32x4 few_stream(const uint8_t* __restrict__ w, const
   for (int i = 0; i < n; i += U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (i + u < n) {
-        if constexpr (MX) acc = mfma_mx<0, 0>(ra[u], rb[u], acc, sa[u], sb[u]);
-        else acc = mfma16x16x32(ra[u], rb[u], acc);
-      }
+      if (i + u < n) acc = mfma16x16x32(ra[u], rb[u], acc);
       load(u, i + u + U);
     }
   }
@@ -123,8 +110,7 @@ __device__ __forceinline__ void few_logits_bf16(const FewArgs& A, int job) {
   const int ks = A.d / A.splits / 32, kb0 = sp * ks;
   const uint16_t* w = static_cast<const uint16_t*>(A.wg) + frag_offset(eb, kb0, A.d / 32) + lane * 8;
   const uint16_t* xr = static_cast<const uint16_t*>(A.x) + static_cast<size_t>(min(r, A.T - 1)) * A.d + kb0 * 32 + g * 8;
-  const f32x4 acc = few_stream<false, 16>(reinterpret_cast<const uint8_t*>(w), reinterpret_cast<const uint8_t*>(xr), 64,
-                                          nullptr, nullptr, 0, ks);
+  const f32x4 acc = few_stream<16>(reinterpret_cast<const uint8_t*>(w), reinterpret_cast<const uint8_t*>(xr), ks);
   if (r < A.T) {
     float* o = A.partial + (static_cast<size_t>(sp) * A.T + r) * A.E;
 #pragma unroll

@@ -17,8 +17,8 @@ namespace {
 // token column, so the block's largest magnitude takes two lane exchanges.
 // `a` is quantised from fp32, without a rounding to bf16 in between.  Codes
 // (two bytes a lane and row block pair) and scales are staged in LDS.
-// store(t, blk) gives the staged place of tile row t, block blk of the tile:
-// 16 bytes of codes, and the scale byte.
+// code(t, blk) and scale(t, blk) give the staged places of tile row t, block
+// blk of the tile: 16 bytes of codes, and the scale byte.
 template <class C, bool GATED, class Code, class Scale>
 __device__ __forceinline__ void mx_quantize_act(const MxAcc<C>& acc, int count, Code code, Scale scale) {
   constexpr int RB = GATED ? 4 : 2;             // row blocks per 32 intermediate indices

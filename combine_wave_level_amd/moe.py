@@ -581,10 +581,11 @@ FEW_MAX_TOKENS = 16
 
 
 def forward_few(p: Problem, x, packed, ws, bias=None, want_logits=False, mxfp4=False, out=None):
-    """The whole layer for at most FEW_MAX_TOKENS tokens: the results of
-    forward (packed from pack_weights) or, with mxfp4=True, of forward_mxfp4
-    (packed from pack_weights_mxfp4), bit for bit, in fewer and shorter
-    kernels.  Returns idx, w, logits and out."""
+    """The whole layer for at most FEW_MAX_TOKENS tokens, in fewer and shorter
+    kernels: forward (packed from pack_weights) or, with mxfp4=True,
+    forward_mxfp4 (packed from pack_weights_mxfp4).  idx, w and logits are
+    theirs bit for bit; out lacks one rounding of theirs (the pairs' y stay
+    in fp32 up to the weighted sum).  Returns idx, w, logits and out."""
     _need("x", x, (p.T, p.d), _TORCH_DTYPE[p.x_dtype])
     _need("packed", packed, (packed_mxfp4_size(p) if mxfp4 else packed_weights_size(p),), torch.uint8)
     _need_workspace(p, ws)

@@ -321,7 +321,8 @@ moe_status_t moe_expert_ffn_waved_fp8(const moe_problem_t* p, const uint8_t* x_f
  * already are MXFP4 values of their block stay what they are.  A block that
  * holds an infinity or a NaN gets scale byte 255 and codes 0 and reads as NaN
  * throughout.  (A value above 3.5 * 2^126 rounds to 4 * 2^126, which an fp32
- * or bf16 reader sees as infinity.)  The caller may bring codes and scales of any other rule.
+ * or bf16 reader sees as infinity.)  The caller may bring codes and scales of
+ * any other rule.
  *
  * Token rows of d elements: codes in moe_mxfp4_codes_stride(d) bytes a row
  * (d / 2 rounded up to 128), scales in moe_mxfp4_scales_stride(d) bytes a row
@@ -372,19 +373,21 @@ moe_status_t moe_unpack_weights_mxfp4(const moe_problem_t* p, const void* packed
  *   there.  packed: from moe_pack_weights_mxfp4.  The rest as
  *   moe_expert_ffn_waved (same workspace after moe_dispatch); y also serves as
  *   scratch, so its rows past the routed ones are undefined after the call.
- *   The call runs the phase schedule and may be repeated on one dispatch; calls that
- *   overlap on one workspace race. */
+ *   The call runs the phase schedule and may be repeated on one dispatch;
+ *   calls that overlap on one workspace race. */
 moe_status_t moe_expert_ffn_mxfp4(const moe_problem_t* p, const uint8_t* codes, const uint8_t* scales,
                                   const void* packed, const int32_t* expert_offsets, const int32_t* sorted_token,
                                   const int32_t* pair_pos, const float* topk_w, void* y, void* out, void* ws,
                                   size_t ws_bytes, moe_stream_t stream);
 
 /* The whole layer for a few tokens (a decode step): x to routing and output,
- * without dispatch tables.  The results are those of the composed calls bit
- * for bit: topk_idx, topk_w and logits of moe_route; out of
- * moe_expert_ffn_waved after moe_dispatch (moe_forward_few, packed from
- * moe_pack_weights), or of moe_quantize_mxfp4 and moe_expert_ffn_mxfp4
- * (moe_forward_few_mxfp4, packed from moe_pack_weights_mxfp4).
+ * without dispatch tables.  topk_idx, topk_w and logits are those of moe_route
+ * bit for bit.  out is that of moe_expert_ffn_waved after moe_dispatch
+ * (moe_forward_few, packed from moe_pack_weights), or of moe_quantize_mxfp4
+ * and moe_expert_ffn_mxfp4 (moe_forward_few_mxfp4, packed from
+ * moe_pack_weights_mxfp4), with one rounding less: the pairs' y stay in fp32
+ * up to the combine, where those calls round them to bf16.  A token's results
+ * do not depend on the tokens beside it.
  *   0 <= T <= MOE_FEW_MAX_TOKENS (MOE_ERR_UNSUPPORTED beyond).
  *   x, bias, topk_idx, topk_w, logits (NULL: not written): as moe_route;
  *   out [T, d] in out_dtype.  ws: the forward workspace; nothing in it needs

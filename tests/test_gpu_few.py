@@ -88,6 +88,13 @@ def test_equals_the_composed_path(case, mx):
     Few(T, d, I, E, k, E_local, e_begin, mx=mx, seed=T + d).check()
 
 
+def test_most_pairs_with_two_row_blocks_a_wavefront():
+    """16 tokens of 64 picks in the wider MXFP4 tile: the largest y in LDS."""
+    print("[case] few 1024 pairs", flush=True)
+    Few(16, 1024, 1024, 64, 64, mx=True, seed=7).check()
+    Few(16, 1024, 1024, 256, 64, 96, 96, mx=True, seed=8).check()
+
+
 @pytest.mark.parametrize("mx", [False, True])
 @pytest.mark.parametrize("x,act,out", [("f32", GATED, "f32"), ("f32", UNGATED, "bf16"), ("bf16", UNGATED, "f32"),
                                        ("bf16", GATED, "f32")])
