@@ -179,24 +179,6 @@ __device__ __forceinline__ void mx_mfma(const MxFrags<C>& f, MxAcc<C>& acc, int 
 // ------------------------------------------------------------------ loads and reads of a K step
 
 template <class C>
-__device__ __forceinline__ void mx_issue(const MxWideSrc& s, uint8_t* lds, int kt) {
-  uint8_t* st = lds + (kt % C::NST) * C::STAGE;
-  const size_t fstep = static_cast<size_t>(s.KB) * 1024;
-  const int wave = mx_wave(), lane = lane_id();
-#pragma unroll
-  for (int i = 0; i < C::LW; ++i) {
-    const int f = C::NW * i + wave;
-    lds_dma16(s.w + (f * fstep + static_cast<size_t>(kt) * 1024) + lane * 16, st + f * 1024);
-  }
-#pragma unroll
-  for (int i = 0; i < C::LT; ++i) {
-    const int f = C::NW * i + wave;
-    lds_dma16(s.t + (f * fstep + static_cast<size_t>(kt) * 1024) + lane * 16, st + C::T0 + f * 1024);
-  }
-  lds_dma4(s.scale + static_cast<size_t>(kt) * 256 + lane * 4, st + C::S0 + wave % (C::NQ + C::NQT) * 256);
-}
-
-template <class C>
 __device__ __forceinline__ void mx_issue(const MxStreamSrc<C>& s, uint8_t* lds, int kt) {
   uint8_t* st = lds + (kt % C::NST) * C::STAGE;
   const int wave = mx_wave(), lane = lane_id();
@@ -218,17 +200,13 @@ template <class C>
 __device__ __forceinline__ void mx_read(const uint8_t* st, MxFrags<C>& f, int nbv) {
   const int lane = lane_id(), wr = mx_wr<C>(), wt = mx_wt<C>();
   f.sa = *reinterpret_cast<const uint32_t*>(st + C::S0 + wr * 256 + lane * 4);
-  if constexpr (!C::STREAM)  // the wavefront's token blocks are bytes AT * wt % 4 .. of their group's word
-    f.sb[0] = *reinterpret_cast<const uint32_t*>(st + C::S0 + (C::NQ + wt * C::AT / 4) * 256 + lane * 4) >>
-              (8 * (wt * C::AT % 4));
 #pragma unroll
   for (int a = 0; a < C::AW; ++a) f.a[a] = ld16(st + (wr * C::AW + a) * 1024 + lane * 16);
 #pragma unroll
   for (int b = 0; b < C::AT; ++b)
-    if (!C::STREAM || b < nbv) {
-      if constexpr (C::STREAM)
-        f.sb[b] = *reinterpret_cast<const uint32_t*>(st + C::S0 + C::NQ * 256 + ((wt * C::AT + b) * 16 + (lane & 15)) * 4) >>
-                  (8 * (lane >> 4));
+    if (b < nbv) {
+      f.sb[b] = *reinterpret_cast<const uint32_t*>(st + C::S0 + C::NQ * 256 + ((wt * C::AT + b) * 16 + (lane & 15)) * 4) >>
+                (8 * (lane >> 4));
       f.b[b] = ld16(st + C::T0 + (wt * C::AT + b) * 1024 + lane * 16);
     }
 }
@@ -241,10 +219,10 @@ __device__ __forceinline__ void mx_wait_from(int later) {
   }
 }
 
-// ACT false: no row of the wavefront is valid; it loads and waits with the
-// others.
-template <class C, bool ACT, class Src>
-__device__ __forceinline__ void mx_run(const Src& s, uint8_t* lds, MxAcc<C>& acc, int nbv) {
+// The K loop.  ACT false: no row of the wavefront is valid; it loads and waits
+// with the others.
+template <class C, bool ACT>
+__device__ __forceinline__ void mx_run(const MxStreamSrc<C>& s, uint8_t* lds, MxAcc<C>& acc, int nbv) {
   const int nk = s.KB;
 #pragma unroll
   for (int k = 0; k < C::NST - 1; ++k)
@@ -259,6 +237,79 @@ __device__ __forceinline__ void mx_run(const Src& s, uint8_t* lds, MxAcc<C>& acc
       MxFrags<C> f;
       mx_read<C>(lds + (kt % C::NST) * C::STAGE, f, nbv);
       mx_mfma<C>(f, acc, nbv);
+    }
+    // the reads of this stage are complete before the next barrier frees it
+    wait_lgkm0();
+  }
+  raw_barrier();
+}
+
+__device__ __forceinline__ const uint8_t* mx_uniform(const uint8_t* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  return reinterpret_cast<const uint8_t*>(static_cast<uint64_t>(static_cast<uint32_t>(uniform(static_cast<int>(v)))) |
+                                          static_cast<uint64_t>(static_cast<uint32_t>(uniform(static_cast<int>(v >> 32)))) << 32);
+}
+
+template <class C, bool ACT>
+__device__ __forceinline__ void mx_run(const MxWideSrc& s, uint8_t* lds, MxAcc<C>& acc, int) {
+  const int nk = s.KB, wave = mx_wave(), wr = mx_wr<C>(), wt = mx_wt<C>();
+  const size_t fstep = static_cast<size_t>(nk) * 1024;
+  const uint32_t lane = lane_id();
+  const uint8_t *gw[C::LW], *gt[C::LT], *gs = mx_uniform(s.scale);
+#pragma unroll
+  for (int i = 0; i < C::LW; ++i) gw[i] = mx_uniform(s.w + (C::NW * i + wave) * fstep);
+#pragma unroll
+  for (int i = 0; i < C::LT; ++i) gt[i] = mx_uniform(s.t + (C::NW * i + wave) * fstep);
+  uint8_t *in = lds + wave * 1024, *ins = lds + C::S0 + wave % (C::NQ + C::NQT) * 256;
+  int fill = 0, use = 0;  // stage offsets
+  const auto wrap = [](int o) { return o == (C::NST - 1) * C::STAGE ? 0 : o + C::STAGE; };
+  const auto issue = [&]() {
+#pragma unroll
+    for (int i = 0; i < C::LW; ++i) {
+      lds_dma16(gw[i] + lane * 16u, in + fill + C::NW * i * 1024);
+      gw[i] += 1024;
+    }
+#pragma unroll
+    for (int i = 0; i < C::LT; ++i) {
+      lds_dma16(gt[i] + lane * 16u, in + fill + C::T0 + C::NW * i * 1024);
+      gt[i] += 1024;
+    }
+    lds_dma4(gs + lane * 4u, ins + fill);
+    gs += 256;
+    fill = wrap(fill);
+  };
+#pragma unroll
+  for (int k = 0; k < C::NST - 1; ++k)
+    if (k < nk) issue();
+  const uint8_t *la = lds + wr * C::AW * 1024 + lane * 16, *lb = lds + C::T0 + wt * C::AT * 1024 + lane * 16;
+  const uint8_t *lsa = lds + C::S0 + wr * 256 + lane * 4;
+  const uint8_t *lsb = lds + C::S0 + (C::NQ + wt * C::AT / 4) * 256 + lane * 4;
+  for (int kt = 0; kt < nk; ++kt) {
+    const int later = min(C::NST - 2, nk - 1 - kt);
+    if (later <= 0) wait_vmcnt<0>();
+    else mx_wait_from<C, 1>(later);
+    raw_barrier();  // step kt is in LDS, and every wavefront has read step kt - 1
+    MxFrags<C> f;
+    if constexpr (ACT) {
+      f.sa = *reinterpret_cast<const uint32_t*>(lsa + use);
+      f.sb[0] = *reinterpret_cast<const uint32_t*>(lsb + use);
+      f.b[0] = ld16(lb + use);
+#pragma unroll
+      for (int a = 0; a < C::AW; ++a) f.a[a] = ld16(la + use + a * 1024);
+#pragma unroll
+      for (int b = 1; b < C::AT; ++b) f.b[b] = ld16(lb + use + b * 1024);
+      use = wrap(use);
+      // all reads are under way before the first product: left alone, the
+      // compiler reads a token block once the products of the one before are
+      // issued, and the wavefront waits out LDS three times a step
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (kt + C::NST - 1 < nk) issue();
+    if constexpr (ACT) {
+      // the wavefront's token blocks are bytes AT * wt % 4 .. of their group's word
+      f.sb[0] >>= 8 * (wt * C::AT % 4);
+      mx_mfma<C>(f, acc, C::AT);
+      __builtin_amdgcn_sched_barrier(0);
     }
     // the reads of this stage are complete before the next barrier frees it
     wait_lgkm0();
