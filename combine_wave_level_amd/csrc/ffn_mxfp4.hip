@@ -327,10 +327,10 @@ hipError_t launch_ffn_mxfp4(const moe_problem_t& p, const WsLayout& L, const uin
   const uint8_t* base = static_cast<const uint8_t*>(packed);
   // The matrix-bound tiles from 64 rows an expert on the average.  Measured,
   // quantisation to combine, MxWide against MxStream: d = 4096, I = 1024, 16
-  // experts: 49 against 40 us at 48 rows, 53.5 against 54.4 at 64, 58 against
-  // 60 at 96; d = 7168, I = 2048, 32 experts: 179 against 173, 190 against
-  // 251, 206 against 340; d = 2048, I = 768, 64 experts: 63 against 53, 69
-  // against 74, 76 against 89.  And where their operands fit: the activations
+  // experts: 48 against 40 us at 48 rows, 51 against 55 at 64, 55 against 61
+  // at 96; d = 7168, I = 2048, 32 experts: 183 against 171, 191 against 253,
+  // 206 against 339; d = 2048, I = 768, 64 experts: 61 against 54, 66 against
+  // 74, 73 against 91.  And where their operands fit: the activations
   // in 4 bits take the place of the bf16 ones (2 I bytes a row of P_max).
   // MxStream: rows of at most I / 2 + 64 code and I / 32 + 12 scale bytes.
   // MxWide: fragments over the padded rows (and the up to 64 rows that the

@@ -27,8 +27,12 @@
 //   experts of about 1024 rows, 2048 weight rows) take the time of three
 //   (that layer's two products: 165 and 90 us with token lines, 129 and 82
 //   with fragments, 95 and 73 with this tile; 4 wavefronts of 128 x 64 in its
-//   place 105 and 74).  What binds it: 102 KiB of loads in flight a CU
-//   against two to three microseconds until they arrive.
+//   place 105 and 74; 81 and 73 with a step's LDS reads all under way before
+//   its products).  What binds it: the matrix units are busy 39% and 19% of
+//   the time, LDS 24% and 17%; loads and barriers without reads and products
+//   take 61 and 67 us, and the two parts overlap only in part.  Storing y
+//   costs the second product 25 us.  The next tile's loads issued before the
+//   epilogue, y stored without the LDS stage: no gain.
 // MxStream (a few rows an expert, bound by the weights' bytes): 128 x 64, 4
 //   wavefronts of 64 x 32, token rows gathered by the tile, all operands in 4
 //   stages of one K step; three workgroups a CU, so that some load while
@@ -244,6 +248,7 @@ __device__ __forceinline__ void mx_run(const MxStreamSrc<C>& s, uint8_t* lds, Mx
   raw_barrier();
 }
 
+// A wave-uniform pointer in scalar registers.
 __device__ __forceinline__ const uint8_t* mx_uniform(const uint8_t* p) {
   const uint64_t v = reinterpret_cast<uint64_t>(p);
   return reinterpret_cast<const uint8_t*>(static_cast<uint64_t>(static_cast<uint32_t>(uniform(static_cast<int>(v)))) |
